@@ -46,6 +46,7 @@
 #ifndef TL_NVFP4_H
 #define TL_NVFP4_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -334,6 +335,117 @@ tl_status tl_fp8_head(const void* x, int M, const void* w_fp8, int N, int K, flo
 #define TL_GDN_MAX_PATH 32
 tl_status tl_gdn_commit(float* state, int H, int d_k, int d_v, const float* k, const float* v, const float* alpha,
                         const float* beta, int n_nodes, const int* path, int L, void* stream);
+
+/* The 8-bit paged KV cache of the verify pass: slot maps, commits and tree attention.
+ *
+ * 16 of the served model's 64 layers are attention layers (TandemLLM docs v0.12.0, "What TandemLLM
+ * is", section 1.1); the pages do not give the layout of their keys and values. Here they live in a
+ * pool of pages of P tokens; a request's tokens lie in the pages that its row of the block table
+ * names, token t at place t % P of page table[t / P]. A page holds, per KV head, E4M3 bytes of K and
+ * of V and one scale for each (value = e4m3(byte) * scale):
+ *   pages   uint8 [n_pages][n_kv_heads][2][P * D], 16-byte aligned
+ *             side 0, K: [D/16][P][16] (16 consecutive channels of a token are consecutive bytes)
+ *             side 1, V: [P/16][D][16] (16 consecutive tokens of a channel are consecutive bytes)
+ *   scales  float [n_pages][n_kv_heads][2], 8-byte aligned: positive powers of two in 2^-60 .. 2^60
+ *             (tl_kv_commit() writes them; what a page held before its first commit is never used)
+ * One pool serves one layer; layers share block tables and slot maps. */
+typedef struct {
+    void* pages;
+    float* scales;
+    int n_pages;      /* >= 1, n_pages * page_tokens < 2^31 */
+    int page_tokens;  /* P: 16, 32, 64 or 128 */
+    int n_kv_heads;   /* 1..256 */
+    int head_dim;     /* D: 64 or 128 */
+} tl_kv_cache;
+
+#define TL_KV_MAX_BATCH 1024  /* requests of one call */
+#define TL_KV_MAX_ROWS 32     /* new rows (tree nodes) of one request */
+#define TL_KV_MAX_GROUP 16    /* query heads of one KV head */
+
+/* Block tables and slot maps, on the GPU, from the lengths that requests hold and shall hold.
+ *
+ * Request b holds lens[b] tokens in its first ceil(lens[b] / P) pages and shall hold want[b]. A
+ * request that grows takes pages off the stack of free pages; one that shrinks (0: it ended) puts
+ * its last pages back on it, and -1 in its table. All returns come before all takes. In request
+ * order, and within a request by place: the j-th of R pages returned goes to free_pages[n + R - 1 - j]
+ * (n: the stack's height before), and the i-th page taken is free_pages[n + R - 1 - i], so shrinking
+ * back undoes a growth, pages, stack and table. Each token that a request grows by gets a slot,
+ * page * P + place: request b's are slots[starts[b] .. starts[b+1]-1] in order of position; the rest
+ * of `slots` is -1.
+ *   lens        device int [B], in and out (want[b] where the request moved)
+ *   want        device int [B], may not overlap the outputs
+ *   B           1..TL_KV_MAX_BATCH
+ *   page_tokens 16, 32, 64 or 128
+ *   table       device int [B][table_width], in and out; entries behind a request's pages are not read
+ *   free_pages  device int [n_pages], in and out: the stack, its top at n_free[0] - 1
+ *   n_pages     pages of the pool; n_pages * page_tokens < 2^31
+ *   n_free      device int [1], in and out
+ *   slots       device int [max_slots], output (max_slots >= 0)
+ *   starts      device int [B + 1], output
+ *   info        device int [4], output: {code, pages missing, slots missing, requests refused}
+ * The code is 0, or a sum of: 1, the stack holds too few pages, and 2, max_slots is too small (in both
+ * cases no request grows; returns still happen); 4, requests were refused (a negative length, or one
+ * over table_width * page_tokens; they stay as they are); 8, the stack's height is negative or would
+ * pass n_pages (nothing changes). One launch, no workspace. Asynchronous on `stream`. */
+tl_status tl_kv_slots(int* lens, const int* want, int B, int page_tokens, int* table, int table_width,
+                      int* free_pages, int n_pages, int* n_free, int* slots, int max_slots, int* starts, int* info,
+                      void* stream);
+
+/* Commit of accepted tokens into the cache: the attention layers' counterpart of tl_gdn_commit().
+ *
+ * Token i (row src[i] of k and v, or row i) goes to slots[i] = page * P + place. Consecutive tokens
+ * with consecutive places of one page are quantised together: with a the largest finite magnitude of
+ * their values in a head and side,
+ *   e = the smallest whole number in -60 .. 60 with a <= 448 * 2^e;
+ *   if place 0 is among them, the page's scale becomes 2^e; else e is raised to the page's present
+ *   exponent e0 if that is larger, and where it is not, the bytes in front of them are rounded
+ *   to E4M3_RNE(e4m3(byte) * 2^(e0 - e)), exact unless a value becomes subnormal;
+ *   bytes = E4M3_RNE(x * 2^-e), magnitudes over 448 (a > 448 * 2^60) to 448; NaN and infinities to NaN.
+ * Bytes behind them stay as they were.
+ *   k, v        device bf16 [n_rows][n_kv_heads][D], rows row_stride elements apart (slices of the QKV
+ *               projection's output will do); 16-byte aligned, row_stride >= n_kv_heads * D, % 8 == 0
+ *   src         NULL, or device int [n]: source rows, each in 0..n_rows-1
+ *   slots       device int [n]; negative: the token goes nowhere. tl_kv_slots() writes them. No slot twice,
+ *               and the slots of one page consecutive and ascending (else its bytes are undefined)
+ *   n           0..2^24 (0 is a no-op); n_rows >= 1, and >= n without src
+ * A slot outside the pool writes nothing and a row outside k and v counts as zeros; both set the device
+ * status word (TL_ERR_DEVICE_FAULT at the next tl_check_device_error()). The pool may not overlap k, v,
+ * src or slots. No workspace. Asynchronous on `stream`. */
+tl_status tl_kv_commit(const tl_kv_cache* cache, const void* k, const void* v, long long row_stride, int n_rows,
+                       const int* src, const int* slots, int n, void* stream);
+
+/* Bytes of workspace that tl_kv_attention() needs for these sizes (host arithmetic only). */
+tl_status tl_kv_attention_workspace(const tl_kv_cache* cache, int n_q_heads, int B, int max_rows, size_t* bytes);
+
+/* Attention of one token or of a draft tree's rows over the cache: the attention layers of a verify pass.
+ *
+ * Row i of request b is node i of its tree (a plain decoding step is a tree of one row). It sees all
+ * lens[b] cached tokens and, of the request's own new rows, those that its mask names; their K and V are
+ * given as they are and are not in the cache yet (commit the accepted ones afterwards):
+ *   out = softmax(scale * q . k) v  over what the row sees, each query head h on KV head h / (Hq / Hkv);
+ *   a row that sees nothing gives zeros. Nothing is read of tokens or nodes that a row does not see.
+ *   q           device bf16 [R][n_q_heads][D], rows q_stride elements apart
+ *   table       device int [B][table_width]; lens device int [B] (counted as 0 when negative, and as
+ *               table_width * P when larger)
+ *   k_new, v_new  device bf16 [R][n_kv_heads][D], rows new_stride apart; both NULL: rows see cached tokens only
+ *   mask        device uint32 [R], bit j: the row sees node j of its request; NULL: row i sees nodes 0..i
+ *   row_start   device int [B + 1]: request b has rows row_start[b]..row_start[b+1]-1; NULL: max_rows rows
+ *               each (R == B * max_rows). Rows of no request are left as they were
+ *   R           rows of q, k_new, v_new, mask and out (0 is a no-op)
+ *   max_rows    1..TL_KV_MAX_ROWS: no request has more
+ *   out         device bf16 [R][n_q_heads][D], rows out_stride apart; may not overlap anything else here
+ *   workspace   device memory, 256-byte aligned, of at least tl_kv_attention_workspace() bytes; its contents mean
+ *               nothing before or after. Calls that may run at the same time need one each
+ * All of q, k_new, v_new and out: 16-byte aligned, strides multiples of 8 that hold a row.
+ * n_q_heads is a multiple of n_kv_heads, at most TL_KV_MAX_GROUP times it; B in 1..TL_KV_MAX_BATCH.
+ * A page id outside the pool is read as page 0, and a request whose rows do not fit R or max_rows is left
+ * out; both set the device status word. The order of all sums is fixed: equal calls give equal bits.
+ * Asynchronous on `stream`; nothing is allocated once tl_init() ran. */
+tl_status tl_kv_attention(const void* q, long long q_stride, int n_q_heads, const tl_kv_cache* cache, const int* table,
+                          int table_width, const int* lens, int B, const void* k_new, const void* v_new,
+                          long long new_stride, const unsigned* mask, const int* row_start, int R, int max_rows,
+                          float scale, void* out, long long out_stride, void* workspace, size_t workspace_bytes,
+                          void* stream);
 
 /* Synchronise `stream`, then report and clear the device status word:
  * TL_OK, TL_ERR_TIMEOUT (a bounded wait ran out) or TL_ERR_DEVICE_FAULT. Also reads and

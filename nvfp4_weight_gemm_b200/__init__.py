@@ -14,7 +14,8 @@ from ._lib import Matrix, TlError, check
 
 __all__ = ["verify_gemm", "verify_gemm_simt", "set_gemm_path", "get_gemm_path", "gemm_path", "PATH_BLOCK_SCALED",
            "PATH_BF16_EXACT", "PATH_EXACT", "verify_stack", "verify_stack_host", "Plan", "dequant",
-           "quantize", "check_device_error", "noalloc_check_error", "fp8_head", "gdn_commit", "init", "num_sms", "Matrix", "TlError"]
+           "quantize", "check_device_error", "noalloc_check_error", "fp8_head", "gdn_commit", "KvCache", "kv_slots", "kv_commit",
+           "kv_attention", "kv_attention_workspace", "init", "num_sms", "Matrix", "TlError"]
 
 
 def _stream(stream):
@@ -212,3 +213,165 @@ def gdn_commit(state, k, v, alpha, beta, path, stream=None):
     check(_lib.lib().tl_gdn_commit(_ptr(state), H, d_k, d_v, _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), n_nodes, arr,
                                    len(p), _stream(stream)))
     return state
+
+
+# ---------------------------------------------------------------- 8-bit paged KV cache
+
+def _expect(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _ints(name, t, shape, device):
+    import torch
+    _expect(t.dtype == torch.int32 and tuple(t.shape) == tuple(shape) and t.is_contiguous() and t.device == device,
+            f"{name}: need a contiguous int32 tensor of shape {tuple(shape)} on {device}, "
+            f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _rows(name, t, heads, dim, device):
+    """The row stride of bf16 rows [n, heads, dim] whose heads lie side by side (any distance between rows)."""
+    import torch
+    _expect(t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[1] == heads and t.shape[2] == dim and t.device == device,
+            f"{name}: need bf16 [rows, {heads}, {dim}] on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    _expect(t.stride(2) == 1 and (heads == 1 or t.stride(1) == dim), f"{name}: the heads of a row must lie side by side")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0) // 8 * 8, heads * dim)
+
+
+class KvCache:
+    """One layer's 8-bit paged KV cache: `pages` uint8 [n_pages, kv_heads, 2, page_tokens * head_dim] (E4M3 bytes; K as
+    [dim/16, tokens, 16], V as [tokens/16, dim, 16]) and `scales` float32 [n_pages, kv_heads, 2] (powers of two).
+    Holds the two tensors; kv_commit() fills them, kv_attention() reads them."""
+
+    def __init__(self, pages, scales, page_tokens: int):
+        import torch
+        _expect(pages.dtype == torch.uint8 and pages.dim() == 4 and pages.shape[2] == 2 and pages.is_contiguous(),
+                "pages: need a contiguous uint8 tensor [n_pages, kv_heads, 2, page_tokens * head_dim]")
+        _expect(page_tokens > 0 and pages.shape[3] % page_tokens == 0, "pages: page_tokens does not divide a page's side")
+        _expect(scales.dtype == torch.float32 and tuple(scales.shape) == tuple(pages.shape[:3]) and scales.is_contiguous()
+                and scales.device == pages.device, "scales: need a contiguous float32 tensor [n_pages, kv_heads, 2] beside pages")
+        self.pages, self.scales, self.page_tokens = pages, scales, int(page_tokens)
+        self.n_pages, self.kv_heads, self.head_dim = pages.shape[0], pages.shape[1], pages.shape[3] // int(page_tokens)
+
+    @classmethod
+    def empty(cls, n_pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
+        """A pool of uninitialised pages (no page is read before a commit began it)."""
+        import torch
+        return cls(torch.empty((n_pages, kv_heads, 2, page_tokens * head_dim), dtype=torch.uint8, device=device),
+                   torch.empty((n_pages, kv_heads, 2), dtype=torch.float32, device=device), page_tokens)
+
+    def _c(self):
+        return _lib.KvCacheC(self.pages.data_ptr(), self.scales.data_ptr(), self.n_pages, self.page_tokens, self.kv_heads,
+                             self.head_dim)
+
+
+def _on(device, stream):
+    """(device guard, stream pointer): the given stream, or the device's current one."""
+    import torch
+    _expect(device.type == "cuda", f"tensors must be on a CUDA device, got {device}")
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    return torch.cuda.device(device), ctypes.c_void_p(s.cuda_stream)
+
+
+def kv_slots(lens, want, table, free_pages, n_free, page_tokens, slots, starts, info, stream=None):
+    """Block tables and slot maps from lengths, on the GPU (tl_kv_slots). Requests go from `lens` to `want` tokens: those
+    that grow take pages off the stack `free_pages` of height `n_free`, those that shrink (0: ended) return theirs.
+
+    All int32 tensors on one device: lens, want [B]; table [B, width]; free_pages [n_pages]; n_free [1]; outputs
+    slots [max_slots] (a slot for every token that requests grow by, then -1), starts [B + 1], info [4]
+    (code, pages missing, slots missing, requests refused). lens, table, free_pages and n_free are updated in place.
+    Returns (slots, starts, info)."""
+    dev = lens.device
+    B = lens.shape[0] if lens.dim() == 1 else -1
+    for name, t, shape in (("lens", lens, (B,)), ("want", want, (B,)), ("n_free", n_free, (1,)), ("starts", starts, (B + 1,)),
+                           ("info", info, (4,)), ("slots", slots, (slots.numel(),)), ("free_pages", free_pages, (free_pages.numel(),)),
+                           ("table", table, (B, table.shape[-1]))):
+        _ints(name, t, shape, dev)
+    guard, st = _on(dev, stream)
+    with guard:
+        check(_lib.lib().tl_kv_slots(_ptr(lens), _ptr(want), B, page_tokens, _ptr(table), table.shape[1], _ptr(free_pages),
+                                     free_pages.numel(), _ptr(n_free), _ptr(slots), slots.numel(), _ptr(starts), _ptr(info), st))
+    return slots, starts, info
+
+
+def kv_commit(cache, k, v, slots, src=None, stream=None):
+    """Commit accepted tokens into the cache (tl_kv_commit): token i, row src[i] (or i) of k and v, goes to slots[i].
+
+    k, v bf16 [rows, kv_heads, head_dim] (rows may be slices of the QKV projection's output); slots int32 [n] as
+    kv_slots() writes them (negative: nowhere); src int32 [n] or None. Returns `cache`."""
+    dev = cache.pages.device
+    n = slots.numel()
+    stride = _rows("k", k, cache.kv_heads, cache.head_dim, dev)
+    _expect(_rows("v", v, cache.kv_heads, cache.head_dim, dev) == stride and v.shape == k.shape,
+            "k and v must have the same shape and row stride")
+    _ints("slots", slots, (n,), dev)
+    if src is not None:
+        _ints("src", src, (n,), dev)
+    c = cache._c()
+    guard, st = _on(dev, stream)
+    with guard:
+        check(_lib.lib().tl_kv_commit(ctypes.byref(c), _ptr(k), _ptr(v), stride, k.shape[0],
+                                      _ptr(src) if src is not None else None, _ptr(slots), n, st))
+    return cache
+
+
+def kv_attention_workspace(cache, n_q_heads: int, batch: int, max_rows: int) -> int:
+    """Bytes of workspace kv_attention() needs for these sizes."""
+    c, n = cache._c(), ctypes.c_size_t()
+    check(_lib.lib().tl_kv_attention_workspace(ctypes.byref(c), n_q_heads, batch, max_rows, ctypes.byref(n)))
+    return n.value
+
+
+def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_start=None, max_rows=None, scale=None,
+                 out=None, workspace=None, stream=None):
+    """Attention of one token or of a draft tree's rows over the cache (tl_kv_attention).
+
+    q bf16 [R, q_heads, head_dim]; table int32 [B, width], lens int32 [B]: each request's pages and cached tokens;
+    k_new, v_new bf16 [R, kv_heads, head_dim]: the rows' own keys and values, not in the cache yet (None: rows see
+    cached tokens only). mask int32 [R]: bit j, the row sees node j of its request (None: the nodes up to itself).
+    row_start int32 [B + 1]: request b has rows row_start[b]..row_start[b+1]-1, at most max_rows (<= 32) of them
+    (None: R / B rows each). scale defaults to head_dim ** -0.5. out bf16 [R, q_heads, head_dim]; workspace uint8 of
+    kv_attention_workspace() bytes (both allocated when None). Returns `out`."""
+    import torch
+    dev = cache.pages.device
+    R, hq = q.shape[0], q.shape[1]
+    B = lens.shape[0]
+    q_stride = _rows("q", q, hq, cache.head_dim, dev)
+    _ints("lens", lens, (B,), dev)
+    _ints("table", table, (B, table.shape[-1]), dev)
+    if row_start is not None:
+        _ints("row_start", row_start, (B + 1,), dev)
+        _expect(max_rows is not None, "row_start needs max_rows, the most rows of one request")
+    elif max_rows is None:
+        _expect(B > 0 and R % B == 0, f"{R} rows do not go round {B} requests: give row_start")
+        max_rows = R // B
+    if mask is not None:
+        _ints("mask", mask, (R,), dev)
+    new_stride = 0
+    _expect((k_new is None) == (v_new is None), "k_new and v_new go together")
+    if k_new is not None:
+        new_stride = _rows("k_new", k_new, cache.kv_heads, cache.head_dim, dev)
+        _expect(k_new.shape[0] == R and v_new.shape == k_new.shape and
+                _rows("v_new", v_new, cache.kv_heads, cache.head_dim, dev) == new_stride,
+                "k_new and v_new must have q's rows and one row stride")
+    if out is None:
+        out = torch.empty((R, hq, cache.head_dim), dtype=torch.bfloat16, device=dev)
+    out_stride = _rows("out", out, hq, cache.head_dim, dev)
+    _expect(out.shape[0] == R, "out must have q's rows")
+    if R == 0:
+        return out
+    c = cache._c()
+    guard, st = _on(dev, stream)
+    with guard:
+        if workspace is None:
+            workspace = torch.empty(kv_attention_workspace(cache, hq, B, max_rows), dtype=torch.uint8, device=dev)
+            if stream is not None:
+                workspace.record_stream(stream)
+                out.record_stream(stream)
+        check(_lib.lib().tl_kv_attention(
+            _ptr(q), q_stride, hq, ctypes.byref(c), _ptr(table), table.shape[1], _ptr(lens), B,
+            _ptr(k_new) if k_new is not None else None, _ptr(v_new) if v_new is not None else None, new_stride,
+            _ptr(mask) if mask is not None else None, _ptr(row_start) if row_start is not None else None, R, max_rows,
+            float(cache.head_dim ** -0.5 if scale is None else scale), _ptr(out), out_stride, _ptr(workspace),
+            workspace.numel(), st))
+    return out

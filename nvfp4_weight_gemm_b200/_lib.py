@@ -27,7 +27,7 @@ EXPORTS = (
     "tl_nvfp4_plan_run", "tl_nvfp4_plan_run_host", "tl_nvfp4_plan_destroy", "tl_nvfp4_dequant",
     "tl_nvfp4_quantize", "tl_check_device_error", "tl_selftest_bounded_wait", "tl_num_sms", "tl_status_string",
     "tl_last_error_message", "tl_set_gemm_path", "tl_get_gemm_path", "tl_noalloc_check_error", "tl_fp8_head",
-    "tl_gdn_commit",
+    "tl_gdn_commit", "tl_kv_slots", "tl_kv_commit", "tl_kv_attention", "tl_kv_attention_workspace",
 )
 
 # Tensor-core paths (tl_set_gemm_path).
@@ -56,6 +56,14 @@ class Matrix(ctypes.Structure):
     ]
 
 
+class KvCacheC(ctypes.Structure):
+    """tl_kv_cache."""
+    _fields_ = [
+        ("pages", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+        ("page_tokens", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+    ]
+
+
 _lib = None
 
 
@@ -66,6 +74,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m nvfp4_weight_gemm_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         vp, i, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+        ll, sz, kv = ctypes.c_longlong, ctypes.c_size_t, ctypes.POINTER(KvCacheC)
         sig = {
             "tl_init": [i],
             "tl_shutdown": [],
@@ -84,6 +93,10 @@ def lib() -> ctypes.CDLL:
             "tl_noalloc_check_error": [vp],
             "tl_fp8_head": [vp, i, vp, i, i, f, vp, vp, vp, vp],
             "tl_gdn_commit": [vp, i, i, i, vp, vp, vp, vp, i, ctypes.POINTER(i), i, vp],
+            "tl_kv_slots": [vp, vp, i, i, vp, i, vp, i, vp, vp, i, vp, vp, vp],
+            "tl_kv_commit": [kv, vp, vp, ll, i, vp, vp, i, vp],
+            "tl_kv_attention_workspace": [kv, i, i, i, ctypes.POINTER(sz)],
+            "tl_kv_attention": [vp, ll, i, kv, vp, i, vp, i, vp, vp, ll, vp, vp, i, i, f, vp, ll, vp, sz, vp],
             "tl_selftest_bounded_wait": [ctypes.c_uint, vp],
             "tl_num_sms": [i],
             "tl_status_string": [i],

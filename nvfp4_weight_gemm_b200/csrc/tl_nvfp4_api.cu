@@ -27,6 +27,8 @@
 #include "xprep.cuh"
 #include "gemm_bs.cuh"
 #include "kernels_aux.cuh"
+#include "kv_attention.cuh"
+#include "kv_cache.cuh"
 
 namespace {
 
@@ -1218,6 +1220,91 @@ tl_status launch_gdn(float* state, int H, const float* k, const float* v, const 
     return launch_gdn_l<DK, DV, 32>(state, H, k, v, alpha, beta, p, L, stream);
 }
 
+// ---------------------------------------------------------------- 8-bit paged KV cache
+
+int log2_of(int v) { return v == 16 ? 4 : v == 32 ? 5 : v == 64 ? 6 : v == 128 ? 7 : -1; }
+
+size_t kv_pages_bytes(const tl_kv_cache& c) { return (size_t)c.n_pages * c.n_kv_heads * 2 * c.page_tokens * c.head_dim; }
+size_t kv_scales_bytes(const tl_kv_cache& c) { return (size_t)c.n_pages * c.n_kv_heads * 2 * sizeof(float); }
+
+tl_status check_kv_sizes(const tl_kv_cache* c) {
+    if (!c) return fail(TL_ERR_INVALID_VALUE, "null cache");
+    if (log2_of(c->page_tokens) < 0)
+        return fail(TL_ERR_UNSUPPORTED, "page_tokens = %d: must be 16, 32, 64 or 128", c->page_tokens);
+    if (c->head_dim != 64 && c->head_dim != 128)
+        return fail(TL_ERR_UNSUPPORTED, "head_dim = %d: must be 64 or 128", c->head_dim);
+    if (c->n_kv_heads < 1 || c->n_kv_heads > 256)
+        return fail(TL_ERR_INVALID_VALUE, "n_kv_heads = %d outside 1..256", c->n_kv_heads);
+    if (c->n_pages < 1 || (long long)c->n_pages * c->page_tokens > 0x7FFFFFFFll)
+        return fail(TL_ERR_INVALID_VALUE, "n_pages = %d: need n_pages >= 1 and fewer than 2^31 tokens", c->n_pages);
+    return TL_OK;
+}
+
+tl_status check_kv_cache(const tl_kv_cache* c) {
+    tl_status st = check_kv_sizes(c);
+    if (st != TL_OK) return st;
+    if (!c->pages || !c->scales) return fail(TL_ERR_INVALID_VALUE, "null pages or scales");
+    if (!aligned16(c->pages) || (reinterpret_cast<uintptr_t>(c->scales) & 7u))
+        return fail(TL_ERR_MISALIGNED, "pages must be 16-byte and scales 8-byte aligned");
+    return TL_OK;
+}
+
+// Bytes from the first element of the first row to the last of the last.
+size_t strided_bytes(int rows, long long stride, size_t width) {
+    return rows > 0 ? ((size_t)(rows - 1) * (size_t)stride + width) * 2 : 0;
+}
+
+// How an attention call's rows are cut: `nt` rows a tile, `row_tiles` tiles a unit, the parts that can
+// arise on `ctas` CTAs, and the bytes they take.
+constexpr int kKvMaxCtas = 160;   // CTAs of the streaming kernel at most (a B200 has 148 SMs)
+struct KvSplit {
+    int nt, row_tiles, groups;
+    size_t o_bytes, ml_bytes;
+};
+KvSplit kv_split(const tl_kv_cache& c, int n_q_heads, int B, int max_rows, int ctas) {
+    KvSplit s;
+    const int rows = max_rows * (n_q_heads / c.n_kv_heads);
+    s.nt = tl::KV_SIMT_NT;
+    s.row_tiles = (rows + s.nt - 1) / s.nt;
+    s.groups = ctas / s.row_tiles;
+    const size_t parts = ((size_t)B * c.n_kv_heads + kKvMaxCtas) * s.row_tiles * s.nt;
+    s.o_bytes = parts * c.head_dim * sizeof(float);
+    s.ml_bytes = parts * sizeof(float2);
+    return s;
+}
+
+tl_status check_kv_heads(const tl_kv_cache& c, int n_q_heads, int B, int max_rows) {
+    if (n_q_heads < 1 || n_q_heads % c.n_kv_heads != 0)
+        return fail(TL_ERR_INVALID_VALUE, "n_q_heads = %d is not a multiple of n_kv_heads = %d", n_q_heads, c.n_kv_heads);
+    if (n_q_heads / c.n_kv_heads > TL_KV_MAX_GROUP)
+        return fail(TL_ERR_UNSUPPORTED, "%d query heads a KV head: at most %d", n_q_heads / c.n_kv_heads, TL_KV_MAX_GROUP);
+    if (B < 1 || B > TL_KV_MAX_BATCH) return fail(TL_ERR_INVALID_VALUE, "B = %d outside 1..%d", B, TL_KV_MAX_BATCH);
+    if (max_rows < 1 || max_rows > TL_KV_MAX_ROWS)
+        return fail(TL_ERR_INVALID_VALUE, "max_rows = %d outside 1..%d", max_rows, TL_KV_MAX_ROWS);
+    return TL_OK;
+}
+
+template <int D>
+tl_status launch_kv_commit(const tl::KvCommitParams& p, int page_tokens, cudaStream_t stream) {
+    const int smem = page_tokens * (D + 8) * 2;
+    TL_CUDA(cudaFuncSetAttribute(tl::kv_commit_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * (D + 8) * 2));
+    const dim3 grid((unsigned)((p.n + p.chunk - 1) / p.chunk), (unsigned)(2 * p.heads));
+    tl::kv_commit_kernel<D><<<grid, tl::KV_COMMIT_THREADS, smem, stream>>>(p);
+    TL_CUDA(cudaGetLastError());
+    return TL_OK;
+}
+
+template <int D>
+tl_status launch_kv_attention(const tl::KvAttnParams& p, cudaStream_t stream) {
+    tl::kv_attention_kernel<D><<<(unsigned)(p.groups * p.row_tiles), tl::KV_TILE, 0, stream>>>(p);
+    TL_CUDA(cudaGetLastError());
+    const int warps = tl::KV_MERGE_THREADS / 32;
+    const dim3 grid((unsigned)p.B, (unsigned)((p.max_rows * p.heads * p.group + warps - 1) / warps));
+    tl::kv_merge_kernel<D><<<grid, tl::KV_MERGE_THREADS, 0, stream>>>(p);
+    TL_CUDA(cudaGetLastError());
+    return TL_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1549,6 +1636,171 @@ tl_status tl_gdn_commit(float* state, int H, int d_k, int d_v, const float* k, c
     else st = launch_gdn<64, 64>(state, H, k, v, alpha, beta, p, L, s);
     (void)d;
     return st;
+}
+
+tl_status tl_kv_slots(int* lens, const int* want, int B, int page_tokens, int* table, int table_width,
+                      int* free_pages, int n_pages, int* n_free, int* slots, int max_slots, int* starts, int* info,
+                      void* stream) {
+    if (B < 1 || B > TL_KV_MAX_BATCH) return fail(TL_ERR_INVALID_VALUE, "B = %d outside 1..%d", B, TL_KV_MAX_BATCH);
+    const int page_log2 = log2_of(page_tokens);
+    if (page_log2 < 0) return fail(TL_ERR_UNSUPPORTED, "page_tokens = %d: must be 16, 32, 64 or 128", page_tokens);
+    if (table_width < 1 || (long long)table_width * page_tokens > 0x3FFFFFFFll)
+        return fail(TL_ERR_INVALID_VALUE, "table_width = %d: need 1 or more and at most 2^30 tokens", table_width);
+    if (n_pages < 1 || (long long)n_pages * page_tokens > 0x7FFFFFFFll)
+        return fail(TL_ERR_INVALID_VALUE, "n_pages = %d: need n_pages >= 1 and fewer than 2^31 tokens", n_pages);
+    if (max_slots < 0) return fail(TL_ERR_INVALID_VALUE, "max_slots = %d is negative", max_slots);
+    if (!lens || !want || !table || !free_pages || !n_free || (max_slots > 0 && !slots) || !starts || !info)
+        return fail(TL_ERR_INVALID_VALUE, "null pointer");
+    {
+        const void* at[8] = {lens, want, table, free_pages, n_free, slots, starts, info};
+        const size_t bytes[8] = {(size_t)B * 4, (size_t)B * 4, (size_t)B * table_width * 4, (size_t)n_pages * 4, 4,
+                                 (size_t)max_slots * 4, (size_t)(B + 1) * 4, 16};
+        for (int i = 0; i < 8; ++i) {
+            if (reinterpret_cast<uintptr_t>(at[i]) & 3u) return fail(TL_ERR_MISALIGNED, "an array is not 4-byte aligned");
+            for (int j = 0; j < i; ++j)
+                if (bytes[i] && bytes[j] && overlap(at[i], bytes[i], at[j], bytes[j]))
+                    return fail(TL_ERR_INVALID_VALUE, "two of the arrays overlap");
+        }
+    }
+    DevState* d = nullptr;
+    tl_status st = current_state(&d);
+    if (st != TL_OK) return st;
+    tl::KvSlotsParams p{lens, want, table, free_pages, n_free, slots, starts, info, B, table_width, page_log2, n_pages,
+                        max_slots};
+    tl::kv_slots_kernel<<<1, tl::KV_SLOTS_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    TL_CUDA(cudaGetLastError());
+    return TL_OK;
+}
+
+tl_status tl_kv_commit(const tl_kv_cache* cache, const void* k, const void* v, long long row_stride, int n_rows,
+                       const int* src, const int* slots, int n, void* stream) {
+    tl_status st = check_kv_cache(cache);
+    if (st != TL_OK) return st;
+    const size_t width = (size_t)cache->n_kv_heads * cache->head_dim;
+    if (n < 0 || n > (1 << 24)) return fail(TL_ERR_INVALID_VALUE, "n = %d outside 0..2^24", n);
+    if (n == 0) return TL_OK;
+    if (n_rows < 1 || (!src && n_rows < n))
+        return fail(TL_ERR_INVALID_VALUE, "n_rows = %d: need 1 or more, and n = %d without src", n_rows, n);
+    if (row_stride < (long long)width || row_stride % 8 != 0)
+        return fail(TL_ERR_INVALID_VALUE, "row_stride = %lld must be a multiple of 8 of at least %zu", row_stride, width);
+    if (!k || !v || !slots) return fail(TL_ERR_INVALID_VALUE, "null pointer");
+    if (!aligned16(k) || !aligned16(v)) return fail(TL_ERR_MISALIGNED, "k and v must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(slots) & 3u) || (reinterpret_cast<uintptr_t>(src) & 3u))
+        return fail(TL_ERR_MISALIGNED, "slots and src must be 4-byte aligned");
+    {
+        const size_t rb = strided_bytes(n_rows, row_stride, width), ib = (size_t)n * 4;
+        const void* out[2] = {cache->pages, cache->scales};
+        const size_t ob[2] = {kv_pages_bytes(*cache), kv_scales_bytes(*cache)};
+        for (int i = 0; i < 2; ++i)
+            if (overlap(out[i], ob[i], k, rb) || overlap(out[i], ob[i], v, rb) || overlap(out[i], ob[i], slots, ib) ||
+                (src && overlap(out[i], ob[i], src, ib)))
+                return fail(TL_ERR_INVALID_VALUE, "the cache overlaps the inputs");
+        if (overlap(out[0], ob[0], out[1], ob[1])) return fail(TL_ERR_INVALID_VALUE, "pages overlap scales");
+    }
+    DevState* d = nullptr;
+    st = current_state(&d);
+    if (st != TL_OK) return st;
+    tl::KvCommitParams p{static_cast<uint8_t*>(cache->pages), cache->scales, static_cast<const __nv_bfloat16*>(k),
+                         static_cast<const __nv_bfloat16*>(v), src, slots, d->err, row_stride, n_rows, n, cache->n_pages,
+                         log2_of(cache->page_tokens), cache->n_kv_heads, 1};
+    // a few tokens: a CTA each, for latency; a prompt: about a page's tokens each, so that few CTAs find nothing to begin
+    p.chunk = n <= 1024 ? 1 : cache->page_tokens;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cache->head_dim == 128 ? launch_kv_commit<128>(p, cache->page_tokens, s)
+                                  : launch_kv_commit<64>(p, cache->page_tokens, s);
+}
+
+tl_status tl_kv_attention_workspace(const tl_kv_cache* cache, int n_q_heads, int B, int max_rows, size_t* bytes) {
+    tl_status st = check_kv_sizes(cache);
+    if (st != TL_OK) return st;
+    if (!bytes) return fail(TL_ERR_INVALID_VALUE, "null pointer");
+    st = check_kv_heads(*cache, n_q_heads, B, max_rows);
+    if (st != TL_OK) return st;
+    const KvSplit s = kv_split(*cache, n_q_heads, B, max_rows, kKvMaxCtas);
+    *bytes = s.o_bytes + s.ml_bytes;
+    return TL_OK;
+}
+
+tl_status tl_kv_attention(const void* q, long long q_stride, int n_q_heads, const tl_kv_cache* cache, const int* table,
+                          int table_width, const int* lens, int B, const void* k_new, const void* v_new,
+                          long long new_stride, const unsigned* mask, const int* row_start, int R, int max_rows,
+                          float scale, void* out, long long out_stride, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    tl_status st = check_kv_cache(cache);
+    if (st != TL_OK) return st;
+    st = check_kv_heads(*cache, n_q_heads, B, max_rows);
+    if (st != TL_OK) return st;
+    const size_t qw = (size_t)n_q_heads * cache->head_dim, nw = (size_t)cache->n_kv_heads * cache->head_dim;
+    if (table_width < 1 || (long long)table_width * cache->page_tokens > 0x3FFFFFFFll)
+        return fail(TL_ERR_INVALID_VALUE, "table_width = %d: need 1 or more and at most 2^30 tokens", table_width);
+    if (R < 0 || (!row_start && R != B * max_rows))
+        return fail(TL_ERR_INVALID_VALUE, "R = %d: without row_start it is B * max_rows = %d", R, B * max_rows);
+    if (R == 0) return TL_OK;
+    if (!std::isfinite(scale)) return fail(TL_ERR_INVALID_VALUE, "scale is not finite");
+    if (!q || !table || !lens || !out || !workspace) return fail(TL_ERR_INVALID_VALUE, "null pointer");
+    if (!k_new != !v_new) return fail(TL_ERR_INVALID_VALUE, "k_new and v_new go together");
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out))
+        return fail(TL_ERR_MISALIGNED, "q, k_new, v_new and out must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(TL_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+    if (((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(mask) |
+          reinterpret_cast<uintptr_t>(row_start)) & 3u) != 0)
+        return fail(TL_ERR_MISALIGNED, "table, lens, mask and row_start must be 4-byte aligned");
+    if (q_stride < (long long)qw || q_stride % 8 || out_stride < (long long)qw || out_stride % 8 ||
+        (k_new && (new_stride < (long long)nw || new_stride % 8)))
+        return fail(TL_ERR_INVALID_VALUE, "strides must be multiples of 8 that hold a row (%zu, %zu elements)", qw, nw);
+    const KvSplit most = kv_split(*cache, n_q_heads, B, max_rows, kKvMaxCtas);
+    if (workspace_bytes < most.o_bytes + most.ml_bytes)
+        return fail(TL_ERR_INVALID_VALUE, "workspace of %zu bytes: %zu are needed", workspace_bytes, most.o_bytes + most.ml_bytes);
+    {
+        const size_t nb = strided_bytes(R, new_stride, nw);
+        const void* at[10] = {out, workspace, q, cache->pages, cache->scales, table, lens, row_start, mask, k_new};
+        const size_t bytes[10] = {strided_bytes(R, out_stride, qw), workspace_bytes, strided_bytes(R, q_stride, qw),
+                                  kv_pages_bytes(*cache), kv_scales_bytes(*cache), (size_t)B * table_width * 4, (size_t)B * 4,
+                                  row_start ? (size_t)(B + 1) * 4 : 0, mask ? (size_t)R * 4 : 0, k_new ? nb : 0};
+        for (int i = 0; i < 2; ++i) {
+            for (int j = i + 1; j < 10; ++j)
+                if (bytes[j] && overlap(at[i], bytes[i], at[j], bytes[j]))
+                    return fail(TL_ERR_INVALID_VALUE, "%s overlaps another array", i ? "workspace" : "out");
+            if (v_new && overlap(at[i], bytes[i], v_new, nb))
+                return fail(TL_ERR_INVALID_VALUE, "%s overlaps another array", i ? "workspace" : "out");
+        }
+    }
+    DevState* d = nullptr;
+    st = current_state(&d);
+    if (st != TL_OK) return st;
+    const KvSplit sp = kv_split(*cache, n_q_heads, B, max_rows, d->num_sms < kKvMaxCtas ? d->num_sms : kKvMaxCtas);
+    tl::KvAttnParams p;
+    memset(&p, 0, sizeof p);
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.pages = static_cast<const uint8_t*>(cache->pages);
+    p.scales = cache->scales;
+    p.table = table;
+    p.lens = lens;
+    p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+    p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    p.mask = mask;
+    p.row_start = row_start;
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + sp.o_bytes);
+    p.err = d->err;
+    p.q_stride = q_stride;
+    p.new_stride = new_stride;
+    p.out_stride = out_stride;
+    p.scale = scale * tl::KV_LOG2E;
+    p.B = B;
+    p.width = table_width;
+    p.n_pages = cache->n_pages;
+    p.page_log2 = log2_of(cache->page_tokens);
+    p.heads = cache->n_kv_heads;
+    p.group = n_q_heads / cache->n_kv_heads;
+    p.R = R;
+    p.max_rows = max_rows;
+    p.groups = sp.groups;
+    p.row_tiles = sp.row_tiles;
+    p.nt = sp.nt;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cache->head_dim == 128 ? launch_kv_attention<128>(p, s) : launch_kv_attention<64>(p, s);
 }
 
 tl_status tl_nvfp4_dequant(const void* w_codes, const void* w_scales, float global_scale, float* w_out, int N, int K,
