@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include "gemm_tc.cuh"
 #include "kv_cache.cuh"
 #include "ptx.cuh"
 
@@ -117,137 +118,668 @@ struct KvSegIter {
     }
 };
 
-// The simple form of the streaming kernel: fp32 on CUDA cores, one row tile of 16 rows a CTA.
-constexpr int KV_SIMT_NT = 16;
+// ---------------------------------------------------------------- the streaming kernel
+//
+// Both products run on the tensor cores with the cache as operand A and the rows as operand B, so that
+// few rows cost little (an MMA is 128 tokens or channels times NT rows, NT a multiple of 16):
+//
+//     S^T [token][row]   = K  [token][channel] . Q^T      A = K in tensor memory,  B = Q in shared memory
+//     O^T [channel][row] = V^T [channel][token] . P^T     A = V in tensor memory,  B = P in shared memory
+//
+// K and V become f16 on the way (every E4M3 value is an f16 value). Q rows become f16 after an exact
+// scaling of each by a power of two that brings its largest magnitude into [2^14, 2^15): a bf16 value has 8
+// significant bits, so every element within 2^-24 of that is exact and the others are within 2^-40 of it. P is
+// rounded to f16 (11 bits against the output's 8) after a scaling that leaves 2^-22 of the largest
+// weight normal; the sums l take p before that rounding. S, O and l are fp32.
+//
+// The reference m of a row's weights is kept as long as no log-weight of a tile passes it by more than
+// KV_SLACK; only then (and in a segment's first tile) are the tile's maxima found across lanes, and O and
+// l rescaled. So most tiles need one comparison a score and one vote.
+//
+// Roles (one CTA of 16 warps per SM, 128 registers a thread):
+//   * warp 0        producer: a page's K and V of the head are one contiguous piece, brought in by one bulk copy;
+//                   tiles of 128 tokens, a ring of stages. Scales follow by cp.async.
+//   * warp 1        MMA issuer, one tile ahead with S^T.
+//   * warps 2..3    the rows: Q of the next segment, scaled, to shared memory.
+//   * warps 4..7    converters: K (lane = token), then V (lane = channel), 16 bytes of a lane at a time.
+//   * warps 8..15   softmax: two groups of four warps, half of the rows each, lane = token. A group also reads its
+//                   rows of O (lane = channel) when a segment ends and writes the part.
+// Every mbarrier wait is bounded; after one has run out the others return at once, every role runs to its end
+// (so no named barrier is left waiting), and the status word is set.
 
-template <int D>
-__global__ void __launch_bounds__(KV_TILE) kv_attention_kernel(const KvAttnParams p) {
-    __shared__ int pre[KV_MAX_BATCH + 1];
-    __shared__ float qs[KV_SIMT_NT][D];
-    __shared__ float ps[KV_SIMT_NT][KV_TILE];
-    __shared__ float red[4][KV_SIMT_NT];
-    __shared__ const uint8_t* page_at[KV_TILE / 16];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int P = 1 << p.page_log2;
-    for (int b = tid; b < p.B; b += KV_TILE) pre[b + 1] = kv_tiles(kv_len_of(p, b));
+constexpr float KV_SLACK = 7.0f;       // P is at most 2^(KV_SLACK + KV_P_SHIFT), f16's largest value is 2^16 - 32
+constexpr float KV_P_SHIFT = 8.0f;
+
+template <int D, int NT>
+struct KvCfg {
+    static constexpr int WARPS = 16, THREADS = 32 * WARPS;
+    static constexpr int NH = NT / 2;                          // rows of a softmax group
+    static constexpr int STAGE_BYTES = 2 * KV_TILE * D;
+    static constexpr int Q_BYTES = NT * D * 2;                 // D/64 slabs of [NT][64] f16, 128-byte rows, swizzled
+    static constexpr int P_BYTES = NT * KV_TILE * 2;           // two slabs of [NT][64 tokens]
+    static constexpr int PRE_INTS = KV_MAX_BATCH + 4;
+    static constexpr int SMALL_BYTES = PRE_INTS * 4 + 2 * KV_MAX_BATCH    // tiles in front, rows, last tile's tokens
+                                     + 4 * KV_TILE * 8                    // token scales, four tiles
+                                     + 4 * NT * 4                         // row factors, four segments
+                                     + 3 * NT * 4                         // -m, rescaling factors, sums
+                                     + 2 * 4 * NH * 4                     // a group's four warps' maxima or sums
+                                     + 8 * 8 * 8                          // page scales of the stages
+                                     + 512;                               // barriers
+    static constexpr int FIXED = Q_BYTES + 2 * P_BYTES + SMALL_BYTES + 1024 /*align*/;
+    static constexpr int FIT = (232448 - FIXED) / STAGE_BYTES;
+    static constexpr int STAGES = FIT < 6 ? FIT : 6;
+    static constexpr int SMEM_BYTES = FIXED + STAGES * STAGE_BYTES;
+    static constexpr uint32_t IDESC = idesc_f16(0u /*f16*/, 128u, (uint32_t)NT);
+    // tensor memory columns: two K tiles, two V tiles, two S^T, one O^T
+    static constexpr int K_COL = 0, K_COLS = D / 2;
+    static constexpr int V_COL = 2 * K_COLS, V_COLS = KV_TILE / 2;
+    static constexpr int S_COL = V_COL + 2 * V_COLS;
+    static constexpr int O_COL = S_COL + 2 * NT;
+    static constexpr int TMEM_COLS = 512;
+    static_assert(O_COL + NT <= TMEM_COLS, "tensor memory budget");
+    static_assert(NT % 16 == 0 && NH % 8 == 0, "MMA and store shapes");
+    static_assert(STAGES >= 3 && STAGES <= 8, "shared memory budget");
+};
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"r"(taddr), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+                 : "memory");
+}
+
+// Two fp32 values in one register pair: Blackwell's packed fp32 arithmetic does both in one instruction.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float kv_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float kv_lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float kv_warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void kv_group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool kv_group_any(int id, bool mine) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(id), "r"((uint32_t)mine) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
+    asm volatile("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tst.shared.b16 [%0], t;\n\t}" ::"r"(addr), "r"(v) : "memory");
+}
+// Two f16 values (a in the low half).
+__device__ __forceinline__ uint32_t kv_pack_f16(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Sixteen E4M3 bytes -> eight f16x2 words.
+__device__ __forceinline__ void kv_decode16(uint4 q, uint32_t* out) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(out[2 * j]), "=r"(out[2 * j + 1]) : "r"(w[j]));
+}
+
+__device__ __forceinline__ uint64_t kv_uniform64(uint64_t v) {
+    return ((uint64_t)__shfl_sync(0xFFFFFFFFu, (uint32_t)(v >> 32), 0) << 32) | (uint64_t)__shfl_sync(0xFFFFFFFFu, (uint32_t)v, 0);
+}
+
+// A walk along a CTA's range that leaves out the units whose row tile holds no rows.
+struct KvWalk {
+    KvSegIter it;
+    const uint8_t* rows;      // rows of each request
+    int group, r0;            // query heads of a KV head; first row of this CTA's row tile
+    __device__ __forceinline__ KvWalk(const int* pre, const uint8_t* rows_, const KvAttnParams& p, long long begin, long long end, int r0_)
+        : it(pre, p.B, p.heads, begin, end), rows(rows_), group(p.group), r0(r0_) {}
+    __device__ __forceinline__ bool next(KvSeg& s) {
+        while (it.next(s))
+            if ((int)rows[s.b] * group > r0) return true;
+        return false;
+    }
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(const __grid_constant__ KvAttnParams p) {
+    using C = KvCfg<D, NT>;
+    constexpr int NH = C::NH;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* const q_sm = smem;
+    uint8_t* const p_sm = q_sm + C::Q_BYTES;
+    uint8_t* const stages = p_sm + 2 * C::P_BYTES;
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(stages + C::STAGES * C::STAGE_BYTES);
+    uint64_t* const kvfull = bars;               // [8] a stage's bytes and scales landed
+    uint64_t* const kvempty = kvfull + 8;        // [8] read by the converters
+    uint64_t* const kready = kvempty + 8;        // [2] K tile in tensor memory
+    uint64_t* const qkdone = kready + 2;         // [2] S^T complete (and the K tile free)
+    uint64_t* const sempty = qkdone + 2;         // [2] S^T read by the softmax warps
+    uint64_t* const vready = sempty + 2;         // [2] V tile in tensor memory
+    uint64_t* const pready = vready + 2;         // [2] P in shared memory, O rescaled if need be
+    uint64_t* const pvdone = pready + 2;         // [2] O^T has the tile (and the V tile and P are free)
+    uint64_t* const qready = pvdone + 2;         // [1] Q of a segment in shared memory
+    uint64_t* const qfree = qready + 1;          // [1] its last S^T is complete
+    uint64_t* const ofull = qfree + 1;           // [1] a segment's O^T is complete
+    uint64_t* const oempty = ofull + 1;          // [1] read by the softmax warps
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(oempty + 1);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    float2* const tok = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + 512);   // [4][128] (K scale, V scale)
+    float2* const page_scale = tok + 4 * KV_TILE;                                            // [8 stages][8 pages]
+    float* const rowf = reinterpret_cast<float*>(page_scale + 64);                           // [4][NT] score = S * rowf * K scale
+    float* const negm = rowf + 4 * NT;                                                       // [NT] -m
+    float* const resc = negm + NT;                                                           // [NT]
+    float* const lsum = resc + NT;                                                           // [NT]
+    float* const red = lsum + NT;                                                            // [2][4][NH]
+    int* const pre = reinterpret_cast<int*>(red + 8 * NH);
+    uint8_t* const rows8 = reinterpret_cast<uint8_t*>(pre + C::PRE_INTS);
+    uint8_t* const last8 = rows8 + KV_MAX_BATCH;                                             // tokens of the last tile
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) { mbar_init(&kvfull[i], 33); mbar_init(&kvempty[i], 4); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&kready[i], 4); mbar_init(&qkdone[i], 1); mbar_init(&sempty[i], 8);
+            mbar_init(&vready[i], 4); mbar_init(&pready[i], 8); mbar_init(&pvdone[i], 1);
+        }
+        mbar_init(qready, 2); mbar_init(qfree, 1); mbar_init(ofull, 1); mbar_init(oempty, 8);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    for (int b = threadIdx.x; b < p.B; b += C::THREADS) {
+        int first;
+        bool bad = false;
+        const int len = kv_len_of(p, b);
+        rows8[b] = (uint8_t)kv_rows_of(p, b, &first, &bad);
+        last8[b] = (uint8_t)(len - (kv_tiles(len) - 1) * KV_TILE);
+        pre[b + 1] = kv_tiles(len);
+    }
+    tc_fence_before();
     __syncthreads();
-    if (tid == 0) {
-        pre[0] = 0;
-        for (int b = 0; b < p.B; ++b) pre[b + 1] += pre[b];
+    tc_fence_after();
+    if (warp == 0) {
+        // inclusive scan of the tiles
+        int carry = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int v = (b0 + lane < p.B) ? pre[b0 + lane + 1] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+                if (lane >= d) v += o;
+            }
+            v += carry;
+            if (b0 + lane < p.B) pre[b0 + lane + 1] = v;
+            carry = __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
+        if (lane == 0) pre[0] = 0;
     }
     __syncthreads();
+    const uint32_t tmem = *tmem_slot;
     const long long total = (long long)p.heads * pre[p.B];
     const long long groups = p.groups < total ? p.groups : total;
     const int g = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
-    if (g >= groups) return;
-    KvSegIter it(pre, p.B, p.heads, kv_range_start(g, total, groups), kv_range_start(g + 1, total, groups));
-    KvSeg s;
-    while (it.next(s)) {
-        int first;
-        bool bad = false;
-        const int rows = kv_rows_of(p, s.b, &first, &bad) * p.group;
-        const int r0 = rt * p.nt, n_rows = min(rows - r0, p.nt);
-        if (n_rows <= 0) continue;
-        const int len = kv_len_of(p, s.b);
-        for (int e = tid; e < KV_SIMT_NT * D; e += KV_TILE) {
-            const int n = e / D, d = e % D;
-            float v = 0.0f;
-            if (n < n_rows) {
-                const int i = (r0 + n) / p.group, gq = (r0 + n) % p.group;
-                v = __bfloat162float(p.q[(size_t)(first + i) * p.q_stride + (size_t)(s.head * p.group + gq) * D + d]) * p.scale;
+    const long long t_begin = g < groups ? kv_range_start(g, total, groups) : 0;
+    const long long t_end = g < groups ? kv_range_start(g + 1, total, groups) : 0;
+    KvWalk walk(pre, rows8, p, t_begin, t_end, rt * NT);
+    KvSeg sg;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        const uint64_t pol = p.row_tiles > 1 ? policy_evict_normal() : policy_evict_first();
+        const int per_tile = KV_TILE >> p.page_log2;
+        const uint32_t page_bytes = 2u * D << p.page_log2;
+        const uint32_t stage0 = smem_u32(stages);
+        int s = 0;
+        uint32_t ph = 0, issued = 0, last_ph = 0;
+        bool more = walk.next(sg);
+        int k = more ? sg.k0 : 0;
+        // the page that this lane brings in of tile k: looked up a tile ahead
+        auto look = [&](int& n) -> int {
+            const int len = (sg.tiles - 1) * KV_TILE + last8[sg.b];
+            n = min(((len + (1 << p.page_log2) - 1) >> p.page_log2) - k * per_tile, per_tile);
+            return lane < n ? __ldg(p.table + (size_t)sg.b * p.width + (size_t)k * per_tile + lane) : 0;
+        };
+        int n = 0, id = more ? look(n) : 0;
+        while (more) {
+            const int cur_n = n, head = sg.head;
+            int page = id;
+            if (++k == sg.k1) {
+                more = walk.next(sg);
+                k = sg.k0;
             }
-            qs[n][d] = v;
-        }
-        float o[KV_SIMT_NT], m[KV_SIMT_NT], l[KV_SIMT_NT];
-#pragma unroll
-        for (int n = 0; n < KV_SIMT_NT; ++n) { o[n] = 0.0f; m[n] = -INFINITY; l[n] = 0.0f; }
-        for (int k = s.k0; k < s.k1; ++k) {
-            __syncthreads();
-            const int t = k * KV_TILE + tid;
-            const int blk = min(t, len - 1) >> p.page_log2;
-            int page = p.table[(size_t)s.b * p.width + blk];
+            if (more) id = look(n);
             if (page < 0 || page >= p.n_pages) {
                 atomicCAS(p.err, 0, TL_DEV_ERR_KV_PAGE);
                 page = 0;
             }
-            const uint8_t* const at = p.pages + ((size_t)page * p.heads + s.head) * 2 * ((size_t)P * D);
-            if ((tid & 15) == 0) page_at[tid / 16] = at + (size_t)P * D;
-            const float ks = p.scales[((size_t)page * p.heads + s.head) * 2];
-            const float vs = p.scales[((size_t)page * p.heads + s.head) * 2 + 1];
-            const float lv = log2f(vs);
-            float w[KV_SIMT_NT];
+            if (!__all_sync(0xFFFFFFFFu, tc_wait(&kvempty[s], ph ^ 1u, abort_flag))) {
+                if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_PRODUCER);
+                break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&kvfull[s], page_bytes * (uint32_t)cur_n);
+            __syncwarp();
+            if (lane < cur_n) {
+                const size_t unit = (size_t)page * p.heads + head;
+                bulk_load_s(stage0 + (uint32_t)(s * C::STAGE_BYTES) + page_bytes * (uint32_t)lane, p.pages + unit * page_bytes, page_bytes,
+                            &kvfull[s], pol);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(page_scale + 8 * s + lane)), "l"(p.scales + 2 * unit)
+                             : "memory");
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&kvfull[s])) : "memory");
+            issued |= 1u << s;
+            last_ph = (last_ph & ~(1u << s)) | (ph << s);
+            if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+        }
+        // every issued copy must land before the CTA can leave
+        for (int i = 0; i < C::STAGES; ++i)
+            if ((issued >> i) & 1u)
+                if (!mbar_wait(&kvfull[i], (last_ph >> i) & 1u, TL_WAIT_LIMIT))
+                    if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DRAIN);
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t tmem_u = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint64_t qdesc = kv_uniform64(smem_desc_k_sw128(smem_u32(q_sm)));
+        const uint64_t pdesc = kv_uniform64(smem_desc_k_sw128(smem_u32(p_sm)));
+        const bool leader = elect_one();
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok && !__all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort_flag))) {
+                if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_MMA);
+                ok = false;
+            }
+        };
+        KvWalk ahead = walk;
+        KvSeg sq;
+        bool more_q = ahead.next(sq);
+        int kq = more_q ? sq.k0 : 0;
+        uint32_t nq = 0, segs_q = 0;        // tiles and segments that S^T was issued for
+        auto issue_qk = [&]() {
+            const uint32_t b = nq & 1u, par = (nq >> 1) & 1u;
+            if (kq == sq.k0) wait(qready, segs_q & 1u);
+            wait(&kready[b], par);
+            wait(&sempty[b], par ^ 1u);
+            if (!ok) return;
+            tc_fence_after();
+            const bool last = kq + 1 == sq.k1;
+            if (leader) {
 #pragma unroll
-            for (int n = 0; n < KV_SIMT_NT; ++n) w[n] = 0.0f;
-            for (int c = 0; c < D / 16; ++c) {
-                const uint4 q4 = *reinterpret_cast<const uint4*>(at + ((size_t)c * P + (t & (P - 1))) * 16);
-                const uint32_t in[4] = {q4.x, q4.y, q4.z, q4.w};
+                for (int i = 0; i < D / 16; ++i)
+                    mma_ts_f16(tmem_u + (uint32_t)(C::S_COL) + b * NT, tmem_u + (uint32_t)(C::K_COL + 8 * i) + b * C::K_COLS,
+                               qdesc + (uint64_t)(((i >> 2) * NT * 128 + (i & 3) * 32) >> 4), C::IDESC, i ? 1u : 0u);
+                mma_commit(&qkdone[b]);
+                if (last) mma_commit(qfree);
+            }
+            __syncwarp();
+            ++nq;
+            if (last) {
+                more_q = ahead.next(sq);
+                kq = sq.k0;
+                ++segs_q;
+            } else {
+                ++kq;
+            }
+        };
+        if (more_q) issue_qk();
+        uint32_t np = 0, segs_p = 0;
+        while (ok && walk.next(sg)) {
+            for (int k = sg.k0; ok && k < sg.k1; ++k) {
+                if (more_q) issue_qk();
+                const uint32_t b = np & 1u, par = (np >> 1) & 1u;
+                if (k == sg.k0) wait(oempty, (segs_p & 1u) ^ 1u);
+                wait(&vready[b], par);
+                wait(&pready[b], par);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const uint32_t h = kv_f16x2((in[u >> 1] >> (16 * (u & 1))) & 0xFFFFu);
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-#pragma unroll
-                    for (int n = 0; n < KV_SIMT_NT; ++n)
-                        w[n] = fmaf(f.y, qs[n][16 * c + 2 * u + 1], fmaf(f.x, qs[n][16 * c + 2 * u], w[n]));
+                    for (int i = 0; i < KV_TILE / 16; ++i)
+                        mma_ts_f16(tmem_u + (uint32_t)C::O_COL, tmem_u + (uint32_t)(C::V_COL + 8 * i) + b * C::V_COLS,
+                                   pdesc + (uint64_t)((b * C::P_BYTES + (i >> 2) * NT * 128 + (i & 3) * 32) >> 4), C::IDESC,
+                                   (i || k != sg.k0) ? 1u : 0u);
+                    mma_commit(&pvdone[b]);
+                    if (k + 1 == sg.k1) mma_commit(ofull);
                 }
+                __syncwarp();
+                ++np;
             }
-#pragma unroll
-            for (int n = 0; n < KV_SIMT_NT; ++n) {
-                w[n] = (t < len) ? fmaf(w[n], ks, lv) : -INFINITY;
-                float x = w[n];
-#pragma unroll
-                for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
-                if (lane == 0) red[warp][n] = x;
+            ++segs_p;
+        }
+        // no MMA may still run when tensor memory is released: the last one's barrier
+        if (np > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&pvdone[(np - 1) & 1u], ((np - 1) >> 1) & 1u, TL_WAIT_LIMIT)) && lane == 0)
+            tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DRAIN);
+        if (nq > np && !__all_sync(0xFFFFFFFFu, mbar_wait(&qkdone[(nq - 1) & 1u], ((nq - 1) >> 1) & 1u, TL_WAIT_LIMIT)) && lane == 0)
+            tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DRAIN);
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ rows
+        constexpr int LPR = D / 8;                 // lanes of a row, 8 channels each
+        constexpr int RPP = 64 / LPR;              // rows of a pass
+        const int t = threadIdx.x - 64;
+        const int c = t % LPR;
+        uint32_t seg = 0;
+        while (walk.next(sg)) {
+            const int n_rows = min((int)rows8[sg.b] * p.group - rt * NT, NT);
+            const int first = p.row_start ? __ldg(p.row_start + sg.b) : sg.b * p.max_rows;
+            if (!__all_sync(0xFFFFFFFFu, tc_wait(qfree, (seg & 1u) ^ 1u, abort_flag))) {
+                if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_PRODUCER);
+                break;
             }
-            __syncthreads();
-            float alpha[KV_SIMT_NT];
+#pragma unroll 5
+            for (int n = t / LPR; n < NT; n += RPP) {
+                uint4 q = make_uint4(0, 0, 0, 0);
+                if (n < n_rows) {
+                    const int r = rt * NT + n;
+                    q = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)(first + r / p.group) * p.q_stride +
+                                                             (size_t)(sg.head * p.group + r % p.group) * D) + c);
+                }
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                unsigned top = 0;
 #pragma unroll
-            for (int n = 0; n < KV_SIMT_NT; ++n) {
-                const float top = fmaxf(m[n], fmaxf(fmaxf(red[0][n], red[1][n]), fmaxf(red[2][n], red[3][n])));
-                alpha[n] = (m[n] == -INFINITY) ? 0.0f : exp2f(m[n] - top);
-                m[n] = top;
-                const float pr = (t < len) ? exp2f(w[n] - top) : 0.0f;
-                l[n] = fmaf(l[n], alpha[n], (t < len) ? pr / vs : 0.0f);
-                ps[n][tid] = pr;
+                for (int u = 0; u < 4; ++u) {
+                    const unsigned lo = w[u] & 0x7FFFu, hi = (w[u] >> 16) & 0x7FFFu;
+                    if (lo < 0x7F80u) top = max(top, lo);
+                    if (hi < 0x7F80u) top = max(top, hi);
+                }
+#pragma unroll
+                for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                const int e = min(max((int)(top >> 7) - 127, -100), 127) - 14;
+                const float f = kv_pow2(-e);
+                uint32_t h[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    h[u] = kv_pack_f16(__int_as_float((int)(w[u] << 16)) * f, __int_as_float((int)(w[u] & 0xFFFF0000u)) * f);
+                *reinterpret_cast<uint4*>(q_sm + (c >> 3) * (NT * 128) + n * 128 + (((c & 7) ^ (n & 7)) << 4)) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+                if (c == 0) rowf[(seg & 3u) * NT + n] = p.scale * kv_pow2(e);
             }
-            __syncthreads();
-            if (tid < D) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qready);
+            ++seg;
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------------------ converters
+        const int qd = warp & 3, r = 32 * qd + lane;             // token of the tile; channel
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16);
+        const int pl = p.page_log2;
+        const uint32_t page_bytes = 2u * D << pl;
+        const uint32_t k_off = (uint32_t)(r >> pl) * page_bytes + (uint32_t)(r & ((1 << pl) - 1)) * 16u, k_step = 16u << pl;
+        int s = 0;
+        uint32_t ph = 0, n = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (!__all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort_flag))) {
+                if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DEQUANT);
+                ok = false;
+            }
+        };
+        while (ok && walk.next(sg)) {
+            for (int k = sg.k0; k < sg.k1; ++k) {
+                const uint32_t b = n & 1u, par = (n >> 1) & 1u;
+                wait(&kvfull[s], ph);
+                if (!ok) break;
+                const uint8_t* const st = stages + s * C::STAGE_BYTES;
+                uint4 w[8];
 #pragma unroll
-                for (int n = 0; n < KV_SIMT_NT; ++n) o[n] *= alpha[n];
-                const int valid = min(len - k * KV_TILE, KV_TILE);
-                for (int c = 0; c < (valid + 15) / 16; ++c) {
-                    const int place = (k * KV_TILE + 16 * c) & (P - 1);
-                    const uint4 q4 = *reinterpret_cast<const uint4*>(page_at[c] + ((size_t)(place >> 4) * D + tid) * 16);
-                    const uint32_t in[4] = {q4.x, q4.y, q4.z, q4.w};
+                for (int c = 0; c < D / 16; ++c) w[c] = *reinterpret_cast<const uint4*>(st + k_off + c * k_step);
+                tok[(n & 3u) * KV_TILE + r] = page_scale[8 * s + (r >> pl)];
+                uint32_t out[32];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const uint32_t h = kv_f16x2((in[u >> 1] >> (16 * (u & 1))) & 0xFFFFu);
-                        float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                        const int at_t = 16 * c + 2 * u;
-                        if (at_t >= valid) f.x = 0.0f;
-                        if (at_t + 1 >= valid) f.y = 0.0f;
+                for (int c = 0; c < 4; ++c) kv_decode16(w[c], out + 8 * c);
+                wait(&qkdone[b], par ^ 1u);                       // S^T of the tile two back has read this K tile
+                if (!ok) break;
+                tc_fence_after();
+                tmem_st32(t_lane + (uint32_t)C::K_COL + b * C::K_COLS, out);
+                if (D == 128) {
 #pragma unroll
-                        for (int n = 0; n < KV_SIMT_NT; ++n)
-                            o[n] = fmaf(f.y, ps[n][at_t + 1], fmaf(f.x, ps[n][at_t], o[n]));
+                    for (int c = 0; c < 4; ++c) kv_decode16(w[4 + c], out + 8 * c);
+                    tmem_st32(t_lane + (uint32_t)C::K_COL + b * C::K_COLS + 32u, out);
+                }
+                if (D == 128 || qd < 2) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const int t = 16 * c;
+                        w[c] = *reinterpret_cast<const uint4*>(st + (uint32_t)(t >> pl) * page_bytes + (uint32_t)(D << pl) +
+                                                               (uint32_t)((t & ((1 << pl) - 1)) >> 4) * (16u * D) + 16u * r);
                     }
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) { mbar_arrive(&kvempty[s]); mbar_arrive(&kready[b]); }
+                wait(&pvdone[b], par ^ 1u);                       // O^T of the tile two back has read this V tile
+                if (!ok) break;
+                tc_fence_after();
+                if (D == 128 || qd < 2) {
+                    // tokens behind the request's last one count nothing, whatever their bytes are
+                    const int valid = (k + 1 == sg.tiles) ? last8[sg.b] : KV_TILE;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) kv_decode16(w[4 * half + c], out + 8 * c);
+                        if (valid < KV_TILE) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const int t = 64 * half + 2 * j;
+                                if (t >= valid) out[j] = 0u;
+                                else if (t + 1 >= valid) out[j] &= 0xFFFFu;
+                            }
+                        }
+                        tmem_st32(t_lane + (uint32_t)C::V_COL + b * C::V_COLS + 32u * half, out);
+                    }
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&vready[b]);
+                ++n;
+                if (++s == C::STAGES) { s = 0; ph ^= 1u; }
             }
         }
-        __syncthreads();
-        const size_t slot = ((size_t)s.b * p.heads + s.head + g) * p.row_tiles + rt;
+        tmem_wait_st();
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int grp = (warp - 8) >> 2, qd = warp & 3, t = 32 * qd + lane;      // token of the tile; channel
+        const int c0 = grp * NH, bar_id = 1 + grp;
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16);
+        const uint32_t p_at = smem_u32(p_sm) + (uint32_t)((t >> 6) * (NT * 128) + (((t & 63) >> 3) << 4) + (t & 7) * 2 + c0 * 128);
+        uint32_t n = 0, seg = 0;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            // a failure is recorded and the warp goes on: the group's barriers need all of its warps
+            if (!__all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort_flag)) && lane == 0)
+                tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_EPILOGUE);
+        };
+        while (walk.next(sg)) {
+            float l[NH];
 #pragma unroll
-        for (int n = 0; n < KV_SIMT_NT; ++n) {
-            if (n >= n_rows) break;
-            float x = l[n];
+            for (int i = 0; i < NH; ++i) l[i] = 0.0f;
+            for (int k = sg.k0; k < sg.k1; ++k) {
+                const uint32_t b = n & 1u, par = (n >> 1) & 1u;
+                const bool first = k == sg.k0;
+                wait(&qkdone[b], par);
+                tc_fence_after();
+                float x[NH];
 #pragma unroll
-            for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-            if (lane == 0) red[warp][n] = x;
-            if (tid < D) p.part_o[(slot * p.nt + n) * D + tid] = o[n];
+                for (int i = 0; i < NH; i += 8) tmem_ld8(t_lane + (uint32_t)(C::S_COL + c0 + i) + b * NT, x + i);
+                const float2 sc = tok[(n & 3u) * KV_TILE + t];
+                const int valid = (k + 1 == sg.tiles) ? last8[sg.b] : KV_TILE;
+                const bool live = t < valid;
+                const float vs = live ? sc.y : 1.0f;
+                const float lv = kv_lg2(vs);
+                const uint64_t ks2 = f2_pack(sc.x, sc.x);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sempty[b]);
+                // x = score - m
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NH; i += 4) {
+                    const float4 rf = *reinterpret_cast<const float4*>(rowf + (seg & 3u) * NT + c0 + i);
+                    const float4 nm = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *reinterpret_cast<const float4*>(negm + c0 + i);
+                    f2_unpack(f2_fma(f2_mul(f2_pack(x[i], x[i + 1]), ks2), f2_pack(rf.x, rf.y), f2_pack(nm.x, nm.y)), x[i], x[i + 1]);
+                    f2_unpack(f2_fma(f2_mul(f2_pack(x[i + 2], x[i + 3]), ks2), f2_pack(rf.z, rf.w), f2_pack(nm.z, nm.w)), x[i + 2], x[i + 3]);
+                }
+                if (valid < KV_TILE) {
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) x[i] = live ? x[i] : -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < NH; ++i) top = fmaxf(top, x[i]);
+                if (kv_group_any(bar_id, first || top + lv > KV_SLACK)) {
+                    // the reference moves: maxima of the log-weights over the tile's tokens
+                    float keep = -INFINITY, keep2 = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) {
+                        const float nm = first ? 0.0f : negm[c0 + i];
+                        const float w = kv_warp_max(live ? (x[i] - nm) + lv : -INFINITY);
+                        if (i < 32) keep = (lane == i) ? w : keep;
+                        else keep2 = (lane == i - 32) ? w : keep2;
+                    }
+                    if (lane < NH) red[(grp * 4 + qd) * NH + lane] = keep;
+                    if (NH > 32 && lane < NH - 32) red[(grp * 4 + qd) * NH + 32 + lane] = keep2;
+                    kv_group_sync(bar_id);
+                    if (t < NH) {
+                        const float* const rd = red + grp * 4 * NH + t;
+                        const float old = first ? -INFINITY : -negm[c0 + t];
+                        const float now = fmaxf(old, fmaxf(fmaxf(rd[0], rd[NH]), fmaxf(rd[2 * NH], rd[3 * NH])));
+                        // what x is off by, and what O and l shrink by (nothing is held yet under an old m of minus infinity)
+                        resc[c0 + t] = (old == -INFINITY) ? 0.0f : kv_ex2(old - now);
+                        lsum[c0 + t] = first ? 0.0f : negm[c0 + t];
+                        negm[c0 + t] = -now;
+                    }
+                    kv_group_sync(bar_id);
+                    if (!first) wait(&pvdone[b ^ 1u], ((n - 1) >> 1) & 1u);     // O holds every tile before this one
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < NH; i += 8) {
+                        float o[8];
+                        if (!first) {
+                            tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0 + i), o);
+                            tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float f = resc[c0 + i + j];
+                            x[i + j] = (x[i + j] - lsum[c0 + i + j]) + negm[c0 + i + j];
+                            l[i + j] *= f;
+                            o[j] *= f;
+                        }
+                        if (!first) tmem_st8(t_lane + (uint32_t)(C::O_COL + c0 + i), o);
+                    }
+                    if (!first) tmem_wait_st();
+                    if (valid < KV_TILE) {
+#pragma unroll
+                        for (int i = 0; i < NH; ++i) x[i] = live ? x[i] : -INFINITY;
+                    }
+                }
+                wait(&pvdone[b], par ^ 1u);                       // P's buffer: O^T of the tile two back has read it
+                const float vs8 = vs * 256.0f;                    // 2^KV_P_SHIFT
+                const uint64_t vs2 = f2_pack(vs8, vs8);
+                const uint32_t at = p_at + b * C::P_BYTES;
+#pragma unroll
+                for (int i = 0; i < NH; i += 2) {
+                    const uint64_t e2 = f2_pack(kv_ex2(x[i]), kv_ex2(x[i + 1]));
+                    f2_unpack(f2_add(f2_pack(l[i], l[i + 1]), e2), l[i], l[i + 1]);
+                    float w0, w1;
+                    f2_unpack(f2_mul(e2, vs2), w0, w1);
+                    const uint32_t h = kv_pack_f16(w0, w1);
+                    sts_u16((at ^ (uint32_t)((i & 7) << 4)) + (uint32_t)(i * 128), h);
+                    sts_u16((at ^ (uint32_t)(((i + 1) & 7) << 4)) + (uint32_t)((i + 1) * 128), h >> 16);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pready[b]);
+                ++n;
+            }
+            // the segment's part: l over the lanes and warps, O as it lies
+#pragma unroll
+            for (int i = 0; i < NH; ++i) {
+                float v = l[i];
+#pragma unroll
+                for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+                l[i] = v;
+            }
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < NH; ++i) red[(grp * 4 + qd) * NH + i] = l[i];
+            }
+            const int n_rows = min((int)rows8[sg.b] * p.group - rt * NT, NT);
+            const size_t slot = (((size_t)sg.b * p.heads + sg.head + g) * p.row_tiles + rt) * NT;
+            kv_group_sync(bar_id);
+            if (t < NH && c0 + t < n_rows) {
+                const float* const rd = red + grp * 4 * NH + t;
+                p.part_ml[slot + c0 + t] = make_float2(-negm[c0 + t] - KV_P_SHIFT, 256.0f * ((rd[0] + rd[NH]) + (rd[2 * NH] + rd[3 * NH])));
+            }
+            wait(ofull, seg & 1u);
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < NH; i += 8) {
+                float o[8];
+                tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0 + i), o);
+                tmem_wait_ld();
+                if (D == 128 || qd < 2) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (c0 + i + j < n_rows) p.part_o[(slot + c0 + i + j) * D + t] = o[j];
+                }
+            }
+            tc_fence_before();
+            kv_group_sync(bar_id);            // red and negm may change again
+            if (lane == 0) mbar_arrive(oempty);
+            ++seg;
         }
-        __syncthreads();
-        if (tid < n_rows)
-            p.part_ml[slot * p.nt + tid] = make_float2(0.0f, (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]));
-        if (tid == 0)
-            for (int n = 0; n < n_rows; ++n) p.part_ml[slot * p.nt + n].x = m[n];
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
     }
 }
 

@@ -1264,8 +1264,10 @@ struct KvSplit {
 KvSplit kv_split(const tl_kv_cache& c, int n_q_heads, int B, int max_rows, int ctas) {
     KvSplit s;
     const int rows = max_rows * (n_q_heads / c.n_kv_heads);
-    s.nt = tl::KV_SIMT_NT;
-    s.row_tiles = (rows + s.nt - 1) / s.nt;
+    // the fewest row tiles of at most 80 rows (tensor memory holds no more beside two K and two V tiles), and the
+    // rows dealt out evenly over them in steps of 16, the MMA's
+    s.row_tiles = (rows + 79) / 80;
+    s.nt = ((rows + s.row_tiles - 1) / s.row_tiles + 15) / 16 * 16;
     s.groups = ctas / s.row_tiles;
     const size_t parts = ((size_t)B * c.n_kv_heads + kKvMaxCtas) * s.row_tiles * s.nt;
     s.o_bytes = parts * c.head_dim * sizeof(float);
@@ -1294,10 +1296,23 @@ tl_status launch_kv_commit(const tl::KvCommitParams& p, int page_tokens, cudaStr
     return TL_OK;
 }
 
+template <int D, int NT>
+tl_status launch_kv_stream(const tl::KvAttnParams& p, cudaStream_t stream) {
+    using C = tl::KvCfg<D, NT>;
+    TL_CUDA(cudaFuncSetAttribute(tl::kv_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES));
+    tl::kv_attention_kernel<D, NT><<<(unsigned)(p.groups * p.row_tiles), C::THREADS, C::SMEM_BYTES, stream>>>(p);
+    TL_CUDA(cudaGetLastError());
+    return TL_OK;
+}
+
 template <int D>
 tl_status launch_kv_attention(const tl::KvAttnParams& p, cudaStream_t stream) {
-    tl::kv_attention_kernel<D><<<(unsigned)(p.groups * p.row_tiles), tl::KV_TILE, 0, stream>>>(p);
-    TL_CUDA(cudaGetLastError());
+    tl_status st = p.nt == 16 ? launch_kv_stream<D, 16>(p, stream)
+                 : p.nt == 32 ? launch_kv_stream<D, 32>(p, stream)
+                 : p.nt == 48 ? launch_kv_stream<D, 48>(p, stream)
+                 : p.nt == 64 ? launch_kv_stream<D, 64>(p, stream)
+                              : launch_kv_stream<D, 80>(p, stream);
+    if (st != TL_OK) return st;
     const int warps = tl::KV_MERGE_THREADS / 32;
     const dim3 grid((unsigned)p.B, (unsigned)((p.max_rows * p.heads * p.group + warps - 1) / warps));
     tl::kv_merge_kernel<D><<<grid, tl::KV_MERGE_THREADS, 0, stream>>>(p);
