@@ -96,24 +96,31 @@ struct KvSeg {
 
 struct KvSegIter {
     const int* pre;      // [B + 1] tiles of the requests in front (per head)
-    int B, heads, b;
-    long long t, end;
-    __device__ __forceinline__ KvSegIter(const int* pre_, int B_, int heads_, long long begin, long long end_)
-        : pre(pre_), B(B_), heads(heads_), b(0), t(begin), end(end_) {
-        if (t < end) b = kv_find(pre, B, (int)(t / heads));
+    int heads, b, head, k, left;   // left: tiles to go (a range's share is far below 2^31)
+    __device__ __forceinline__ KvSegIter(const int* pre_, int B, int heads_, long long begin, long long end)
+        : pre(pre_), heads(heads_), b(0), head(0), k(0), left((int)(end - begin)) {
+        if (left <= 0) return;
+        b = kv_find(pre, B, (int)(begin / heads));
+        const int tiles = pre[b + 1] - pre[b];
+        const long long in = begin - (long long)heads * pre[b];
+        head = (int)(in / tiles);
+        k = (int)(in - (long long)head * tiles);
     }
     __device__ __forceinline__ bool next(KvSeg& s) {
-        if (t >= end) return false;
-        while ((long long)heads * pre[b + 1] <= t) ++b;
-        const int tiles = pre[b + 1] - pre[b];
-        const long long in = t - (long long)heads * pre[b];
+        if (left <= 0) return false;
+        int tiles;
+        while ((tiles = pre[b + 1] - pre[b]) == 0) ++b;
         s.b = b;
+        s.head = head;
         s.tiles = tiles;
-        s.head = (int)(in / tiles);
-        s.k0 = (int)(in - (long long)s.head * tiles);
-        const long long left = end - t;
-        s.k1 = (left < tiles - s.k0) ? s.k0 + (int)left : tiles;
-        t += s.k1 - s.k0;
+        s.k0 = k;
+        s.k1 = min(tiles, k + left);
+        left -= s.k1 - k;
+        k = s.k1;
+        if (k == tiles) {
+            k = 0;
+            if (++head == heads) { head = 0; ++b; }
+        }
         return true;
     }
 };
@@ -136,13 +143,15 @@ struct KvSegIter {
 // KV_SLACK; only then (and in a segment's first tile) are the tile's maxima found across lanes, and O and
 // l rescaled. So most tiles need one comparison a score and one vote.
 //
-// Roles (one CTA of 16 warps per SM, 128 registers a thread):
+// Roles (one CTA of 20 warps per SM; registers are moved between the warpgroups, KvCfg):
 //   * warp 0        producer: a page's K and V of the head are one contiguous piece, brought in by one bulk copy;
 //                   tiles of 128 tokens, a ring of stages. Scales follow by cp.async.
-//   * warp 1        MMA issuer, one tile ahead with S^T.
-//   * warps 2..3    the rows: Q of the next segment, scaled, to shared memory.
-//   * warps 4..7    converters: K (lane = token), then V (lane = channel), 16 bytes of a lane at a time.
-//   * warps 8..15   softmax: two groups of four warps, half of the rows each, lane = token. A group also reads its
+//   * warp 1        issues the MMAs of S^T, warp 2 those of O^T (an issuer manages one MMA in some 55 cycles while
+//                   other warps run, so one warp for all sixteen of a tile was a bound).
+//   * warp 3        the rows: Q of the next segment, scaled, to one of two buffers in shared memory. The first
+//                   segment's Q is brought in by the softmax warps, which have nothing to do yet.
+//   * warps 4..7    K converters, lane = token; warps 8..11 V converters, lane = channel; 16 bytes of a lane at a time.
+//   * warps 12..19  softmax: two groups of four warps, half of the rows each, lane = token. A group also reads its
 //                   rows of O (lane = channel) when a segment ends and writes the part.
 // Every mbarrier wait is bounded; after one has run out the others return at once, every role runs to its end
 // (so no named barrier is left waiting), and the status word is set.
@@ -152,29 +161,41 @@ constexpr float KV_P_SHIFT = 8.0f;
 
 template <int D, int NT>
 struct KvCfg {
-    static constexpr int WARPS = 16, THREADS = 32 * WARPS;
+    static constexpr int WARPS = 20, THREADS = 32 * WARPS;
+    // registers a thread: 96 at launch (480 over the five warpgroups), then dealt out by need
+    static constexpr int REGS_CONTROL = 64, REGS_CONVERT = 80, REGS_SOFTMAX = 128;
+    static_assert(REGS_CONTROL + 2 * REGS_CONVERT + 2 * REGS_SOFTMAX <= 480, "registers of the launch");
     static constexpr int NH = NT / 2;                          // rows of a softmax group
     static constexpr int STAGE_BYTES = 2 * KV_TILE * D;
     static constexpr int Q_BYTES = NT * D * 2;                 // D/64 slabs of [NT][64] f16, 128-byte rows, swizzled
     static constexpr int P_BYTES = NT * KV_TILE * 2;           // two slabs of [NT][64 tokens]
     static constexpr int PRE_INTS = KV_MAX_BATCH + 4;
+    // S^T runs up to BUFS tiles (so perhaps BUFS segments) ahead of the softmax, and Q two segments ahead of S^T
+    static constexpr int TOK_RING = 8, ROWF_RING = 8;
     static constexpr int SMALL_BYTES = PRE_INTS * 4 + 2 * KV_MAX_BATCH    // tiles in front, rows, last tile's tokens
-                                     + 4 * KV_TILE * 8                    // token scales, four tiles
-                                     + 4 * NT * 4                         // row factors, four segments
+                                     + TOK_RING * KV_TILE * 8             // token scales
+                                     + ROWF_RING * NT * 4                 // row factors
                                      + 3 * NT * 4                         // -m, rescaling factors, sums
                                      + 2 * 4 * NH * 4                     // a group's four warps' maxima or sums
                                      + 8 * 8 * 8                          // page scales of the stages
                                      + 512;                               // barriers
-    static constexpr int FIXED = Q_BYTES + 2 * P_BYTES + SMALL_BYTES + 1024 /*align*/;
+    // tiles in flight between converters, MMAs and softmax: three where tensor memory holds them
+    static constexpr int BUFS = (3 * (D / 2 + KV_TILE / 2 + NT) + NT <= 512) ? 3 : 2;
+    static_assert(TOK_RING >= 2 * BUFS && ROWF_RING >= BUFS + 3, "rings");
+    static constexpr int FIXED = 2 * Q_BYTES + BUFS * P_BYTES + SMALL_BYTES + 1024 /*align*/;
     static constexpr int FIT = (232448 - FIXED) / STAGE_BYTES;
     static constexpr int STAGES = FIT < 6 ? FIT : 6;
     static constexpr int SMEM_BYTES = FIXED + STAGES * STAGE_BYTES;
     static constexpr uint32_t IDESC = idesc_f16(0u /*f16*/, 128u, (uint32_t)NT);
-    // tensor memory columns: two K tiles, two V tiles, two S^T, one O^T
+    static constexpr uint32_t IDESC_P = IDESC | (1u << 16);    // B = P: rows fastest
+    // P lies token by token, rows fastest (a softmax thread holds one token's rows): atoms of 8 tokens x 16 rows,
+    // 32 bytes a token, 32-byte swizzle; the atoms of 8 tokens side by side, then the next 8 tokens
+    static constexpr int P_ATOM = 256, P_STEP = (NT / 16) * P_ATOM;
+    // tensor memory columns: K tiles, V tiles, S^T, one O^T
     static constexpr int K_COL = 0, K_COLS = D / 2;
-    static constexpr int V_COL = 2 * K_COLS, V_COLS = KV_TILE / 2;
-    static constexpr int S_COL = V_COL + 2 * V_COLS;
-    static constexpr int O_COL = S_COL + 2 * NT;
+    static constexpr int V_COL = BUFS * K_COLS, V_COLS = KV_TILE / 2;
+    static constexpr int S_COL = V_COL + BUFS * V_COLS;
+    static constexpr int O_COL = S_COL + BUFS * NT;
     static constexpr int TMEM_COLS = 512;
     static_assert(O_COL + NT <= TMEM_COLS, "tensor memory budget");
     static_assert(NT % 16 == 0 && NH % 8 == 0, "MMA and store shapes");
@@ -242,8 +263,19 @@ __device__ __forceinline__ bool kv_group_any(int id, bool mine) {
         : "=r"(r) : "r"(id), "r"((uint32_t)mine) : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
-    asm volatile("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tst.shared.b16 [%0], t;\n\t}" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ void sts_128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Shared-memory matrix descriptor of an operand whose rows are fastest, 32-byte swizzle: `mn` bytes between
+// groups of 16 rows, `k` bytes between groups of 8 along the summed axis.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw32(uint32_t saddr, uint32_t mn, uint32_t k) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(mn >> 4) << 16) | ((uint64_t)(k >> 4) << 32) | ((uint64_t)1u << 46) |
+           ((uint64_t)6u << 61);
 }
 // Two f16 values (a in the low half).
 __device__ __forceinline__ uint32_t kv_pack_f16(float a, float b) {
@@ -260,6 +292,16 @@ __device__ __forceinline__ void kv_decode16(uint4 q, uint32_t* out) {
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
             "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
             : "=r"(out[2 * j]), "=r"(out[2 * j + 1]) : "r"(w[j]));
+}
+
+// Bounded wait that also gives up when another role has aborted the CTA. A poll may sleep in hardware for some 20
+// microseconds: the limit is seconds, far beyond any launch.
+__device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    for (uint32_t i = 0; i < (TL_WAIT_LIMIT >> 4); ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+    }
+    return false;
 }
 
 __device__ __forceinline__ uint64_t kv_uniform64(uint64_t v) {
@@ -280,34 +322,95 @@ struct KvWalk {
     }
 };
 
+// Ring position of a tile: buffer and parity of its use.
+template <int N>
+struct KvRing {
+    uint32_t i = 0, par = 0;
+    __device__ __forceinline__ void step() {
+        if (++i == N) { i = 0; par ^= 1u; }
+    }
+};
+
+// The Q rows of a segment's row tile into shared memory as f16, each scaled by a power of two (two K-major slabs of
+// 64 channels, 128-byte swizzle); rowf[n] undoes the scale. By `threads` threads (a multiple of 32), in batches of
+// loads that are all in flight at once.
+template <int D, int NT, int BATCH>
+__device__ __forceinline__ void kv_load_rows(const KvAttnParams& p, const KvSeg& sg, int n_rows, int r0, int t, int threads, uint8_t* q_sm,
+                                             float* rowf) {
+    constexpr int LPR = D / 8;                 // lanes of a row, 8 channels each
+    const int first = p.row_start ? __ldg(p.row_start + sg.b) : sg.b * p.max_rows;
+    const int c = t % LPR, step = threads / LPR;
+    const unsigned inv_group = (65536u + p.group - 1) / p.group;     // r / group = r * inv_group >> 16 for r < 512, group <= 16
+    const __nv_bfloat16* const q0 = p.q + (size_t)first * p.q_stride + (size_t)(sg.head * p.group) * D + 8 * c;
+    for (int n0 = t / LPR; n0 < NT; n0 += BATCH * step) {
+        uint4 q[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int n = n0 + u * step;
+            q[u] = make_uint4(0, 0, 0, 0);
+            if (n < n_rows) {
+                const unsigned r = r0 + n, node = r * inv_group >> 16;
+                q[u] = __ldg(reinterpret_cast<const uint4*>(q0 + (size_t)node * p.q_stride + (size_t)(r - node * p.group) * D));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int n = n0 + u * step;
+            const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+            unsigned top = 0;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const unsigned lo = w[v] & 0x7FFFu, hi = (w[v] >> 16) & 0x7FFFu;
+                if (lo < 0x7F80u) top = max(top, lo);
+                if (hi < 0x7F80u) top = max(top, hi);
+            }
+#pragma unroll
+            for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            if (n < NT) {
+                const int e = min(max((int)(top >> 7) - 127, -100), 127) - 14;
+                const float f = kv_pow2(-e);
+                uint32_t h[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    h[v] = kv_pack_f16(__int_as_float((int)(w[v] << 16)) * f, __int_as_float((int)(w[v] & 0xFFFF0000u)) * f);
+                *reinterpret_cast<uint4*>(q_sm + (c >> 3) * (NT * 128) + n * 128 + (((c & 7) ^ (n & 7)) << 4)) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+                if (c == 0) rowf[n] = p.scale * kv_pow2(e);
+            }
+        }
+    }
+    fence_proxy_async_smem();
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(const __grid_constant__ KvAttnParams p) {
     using C = KvCfg<D, NT>;
     constexpr int NH = C::NH;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    constexpr int BUFS = C::BUFS;
     uint8_t* const q_sm = smem;
-    uint8_t* const p_sm = q_sm + C::Q_BYTES;
-    uint8_t* const stages = p_sm + 2 * C::P_BYTES;
+    uint8_t* const p_sm = q_sm + 2 * C::Q_BYTES;
+    uint8_t* const stages = p_sm + BUFS * C::P_BYTES;
     uint64_t* const bars = reinterpret_cast<uint64_t*>(stages + C::STAGES * C::STAGE_BYTES);
     uint64_t* const kvfull = bars;               // [8] a stage's bytes and scales landed
     uint64_t* const kvempty = kvfull + 8;        // [8] read by the converters
-    uint64_t* const kready = kvempty + 8;        // [2] K tile in tensor memory
-    uint64_t* const qkdone = kready + 2;         // [2] S^T complete (and the K tile free)
-    uint64_t* const sempty = qkdone + 2;         // [2] S^T read by the softmax warps
-    uint64_t* const vready = sempty + 2;         // [2] V tile in tensor memory
-    uint64_t* const pready = vready + 2;         // [2] P in shared memory, O rescaled if need be
-    uint64_t* const pvdone = pready + 2;         // [2] O^T has the tile (and the V tile and P are free)
-    uint64_t* const qready = pvdone + 2;         // [1] Q of a segment in shared memory
-    uint64_t* const qfree = qready + 1;          // [1] its last S^T is complete
-    uint64_t* const ofull = qfree + 1;           // [1] a segment's O^T is complete
+    uint64_t* const kready = kvempty + 8;        // [3] K tile in tensor memory
+    uint64_t* const qkdone = kready + 3;         // [3] S^T complete (and the K tile free)
+    uint64_t* const sempty = qkdone + 3;         // [3] S^T read by the softmax warps
+    uint64_t* const vready = sempty + 3;         // [3] V tile in tensor memory
+    uint64_t* const pready = vready + 3;         // [3] P in shared memory, O rescaled if need be
+    uint64_t* const pvdone = pready + 3;         // [3] O^T has the tile (and the V tile and P are free)
+    uint64_t* const qready = pvdone + 3;         // [2] Q of a segment in shared memory
+    uint64_t* const qfree = qready + 2;          // [2] its last S^T is complete
+    uint64_t* const ofull = qfree + 2;           // [1] a segment's O^T is complete
     uint64_t* const oempty = ofull + 1;          // [1] read by the softmax warps
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(oempty + 1);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    float2* const tok = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + 512);   // [4][128] (K scale, V scale)
-    float2* const page_scale = tok + 4 * KV_TILE;                                            // [8 stages][8 pages]
-    float* const rowf = reinterpret_cast<float*>(page_scale + 64);                           // [4][NT] score = S * rowf * K scale
-    float* const negm = rowf + 4 * NT;                                                       // [NT] -m
+    float2* const tok = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + 512);   // [TOK_RING][128] (K, V scale)
+    float2* const page_scale = tok + C::TOK_RING * KV_TILE;                                  // [8 stages][8 pages]
+    float* const rowf = reinterpret_cast<float*>(page_scale + 64);                           // [ROWF_RING][NT]: score = S * rowf * K scale
+    float* const negm = rowf + C::ROWF_RING * NT;                                                       // [NT] -m
     float* const resc = negm + NT;                                                           // [NT]
     float* const lsum = resc + NT;                                                           // [NT]
     float* const red = lsum + NT;                                                            // [2][4][NH]
@@ -316,13 +419,16 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     uint8_t* const last8 = rows8 + KV_MAX_BATCH;                                             // tokens of the last tile
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the merge may be brought up now; it waits for this launch's parts by itself
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::STAGES; ++i) { mbar_init(&kvfull[i], 33); mbar_init(&kvempty[i], 4); }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::STAGES; ++i) { mbar_init(&kvfull[i], 33); mbar_init(&kvempty[i], 8); }
+        for (int i = 0; i < BUFS; ++i) {
             mbar_init(&kready[i], 4); mbar_init(&qkdone[i], 1); mbar_init(&sempty[i], 8);
             mbar_init(&vready[i], 4); mbar_init(&pready[i], 8); mbar_init(&pvdone[i], 1);
         }
-        mbar_init(qready, 2); mbar_init(qfree, 1); mbar_init(ofull, 1); mbar_init(oempty, 8);
+        for (int i = 0; i < 2; ++i) { mbar_init(&qready[i], 2); mbar_init(&qfree[i], 1); }
+        mbar_init(ofull, 1); mbar_init(oempty, 8);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -367,235 +473,202 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     KvWalk walk(pre, rows8, p, t_begin, t_end, rt * NT);
     KvSeg sg;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        const uint64_t pol = p.row_tiles > 1 ? policy_evict_normal() : policy_evict_first();
-        const int per_tile = KV_TILE >> p.page_log2;
-        const uint32_t page_bytes = 2u * D << p.page_log2;
-        const uint32_t stage0 = smem_u32(stages);
-        int s = 0;
-        uint32_t ph = 0, issued = 0, last_ph = 0;
-        bool more = walk.next(sg);
-        int k = more ? sg.k0 : 0;
-        // the page that this lane brings in of tile k: looked up a tile ahead
-        auto look = [&](int& n) -> int {
-            const int len = (sg.tiles - 1) * KV_TILE + last8[sg.b];
-            n = min(((len + (1 << p.page_log2) - 1) >> p.page_log2) - k * per_tile, per_tile);
-            return lane < n ? __ldg(p.table + (size_t)sg.b * p.width + (size_t)k * per_tile + lane) : 0;
-        };
-        int n = 0, id = more ? look(n) : 0;
-        while (more) {
-            const int cur_n = n, head = sg.head;
-            int page = id;
-            if (++k == sg.k1) {
-                more = walk.next(sg);
-                k = sg.k0;
-            }
-            if (more) id = look(n);
-            if (page < 0 || page >= p.n_pages) {
-                atomicCAS(p.err, 0, TL_DEV_ERR_KV_PAGE);
-                page = 0;
-            }
-            if (!__all_sync(0xFFFFFFFFu, tc_wait(&kvempty[s], ph ^ 1u, abort_flag))) {
-                if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_PRODUCER);
-                break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(&kvfull[s], page_bytes * (uint32_t)cur_n);
-            __syncwarp();
-            if (lane < cur_n) {
-                const size_t unit = (size_t)page * p.heads + head;
-                bulk_load_s(stage0 + (uint32_t)(s * C::STAGE_BYTES) + page_bytes * (uint32_t)lane, p.pages + unit * page_bytes, page_bytes,
-                            &kvfull[s], pol);
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(page_scale + 8 * s + lane)), "l"(p.scales + 2 * unit)
-                             : "memory");
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&kvfull[s])) : "memory");
-            issued |= 1u << s;
-            last_ph = (last_ph & ~(1u << s)) | (ph << s);
-            if (++s == C::STAGES) { s = 0; ph ^= 1u; }
-        }
-        // every issued copy must land before the CTA can leave
-        for (int i = 0; i < C::STAGES; ++i)
-            if ((issued >> i) & 1u)
-                if (!mbar_wait(&kvfull[i], (last_ph >> i) & 1u, TL_WAIT_LIMIT))
-                    if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DRAIN);
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        const uint32_t tmem_u = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-        const uint64_t qdesc = kv_uniform64(smem_desc_k_sw128(smem_u32(q_sm)));
-        const uint64_t pdesc = kv_uniform64(smem_desc_k_sw128(smem_u32(p_sm)));
-        const bool leader = elect_one();
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (ok && !__all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort_flag))) {
-                if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_MMA);
-                ok = false;
-            }
-        };
-        KvWalk ahead = walk;
-        KvSeg sq;
-        bool more_q = ahead.next(sq);
-        int kq = more_q ? sq.k0 : 0;
-        uint32_t nq = 0, segs_q = 0;        // tiles and segments that S^T was issued for
-        auto issue_qk = [&]() {
-            const uint32_t b = nq & 1u, par = (nq >> 1) & 1u;
-            if (kq == sq.k0) wait(qready, segs_q & 1u);
-            wait(&kready[b], par);
-            wait(&sempty[b], par ^ 1u);
-            if (!ok) return;
-            tc_fence_after();
-            const bool last = kq + 1 == sq.k1;
-            if (leader) {
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    mma_ts_f16(tmem_u + (uint32_t)(C::S_COL) + b * NT, tmem_u + (uint32_t)(C::K_COL + 8 * i) + b * C::K_COLS,
-                               qdesc + (uint64_t)(((i >> 2) * NT * 128 + (i & 3) * 32) >> 4), C::IDESC, i ? 1u : 0u);
-                mma_commit(&qkdone[b]);
-                if (last) mma_commit(qfree);
-            }
-            __syncwarp();
-            ++nq;
-            if (last) {
-                more_q = ahead.next(sq);
-                kq = sq.k0;
-                ++segs_q;
-            } else {
-                ++kq;
-            }
-        };
-        if (more_q) issue_qk();
-        uint32_t np = 0, segs_p = 0;
-        while (ok && walk.next(sg)) {
-            for (int k = sg.k0; ok && k < sg.k1; ++k) {
-                if (more_q) issue_qk();
-                const uint32_t b = np & 1u, par = (np >> 1) & 1u;
-                if (k == sg.k0) wait(oempty, (segs_p & 1u) ^ 1u);
-                wait(&vready[b], par);
-                wait(&pready[b], par);
-                if (!ok) break;
-                tc_fence_after();
-                if (leader) {
-#pragma unroll
-                    for (int i = 0; i < KV_TILE / 16; ++i)
-                        mma_ts_f16(tmem_u + (uint32_t)C::O_COL, tmem_u + (uint32_t)(C::V_COL + 8 * i) + b * C::V_COLS,
-                                   pdesc + (uint64_t)((b * C::P_BYTES + (i >> 2) * NT * 128 + (i & 3) * 32) >> 4), C::IDESC,
-                                   (i || k != sg.k0) ? 1u : 0u);
-                    mma_commit(&pvdone[b]);
-                    if (k + 1 == sg.k1) mma_commit(ofull);
+    if (warp < 4) {
+        regs_dec<C::REGS_CONTROL>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer
+            const uint64_t pol = p.row_tiles > 1 ? policy_evict_normal() : policy_evict_first();
+            const int per_tile = KV_TILE >> p.page_log2;
+            const uint32_t page_bytes = 2u * D << p.page_log2;
+            const uint32_t stage0 = smem_u32(stages);
+            int s = 0;
+            uint32_t ph = 0, issued = 0, last_ph = 0;
+            bool more = walk.next(sg);
+            int k = more ? sg.k0 : 0;
+            // the page that this lane brings in of tile k: looked up a tile ahead
+            auto look = [&](int& n) -> int {
+                const int len = (sg.tiles - 1) * KV_TILE + last8[sg.b];
+                n = min(((len + (1 << p.page_log2) - 1) >> p.page_log2) - k * per_tile, per_tile);
+                return lane < n ? __ldg(p.table + (size_t)sg.b * p.width + (size_t)k * per_tile + lane) : 0;
+            };
+            int n = 0, id = more ? look(n) : 0;
+            while (more) {
+                const int cur_n = n, head = sg.head;
+                int page = id;
+                if (++k == sg.k1) {
+                    more = walk.next(sg);
+                    k = sg.k0;
                 }
+                if (more) id = look(n);
+                if (page < 0 || page >= p.n_pages) {
+                    atomicCAS(p.err, 0, TL_DEV_ERR_KV_PAGE);
+                    page = 0;
+                }
+                if (!__all_sync(0xFFFFFFFFu, kv_wait(&kvempty[s], ph ^ 1u, abort_flag))) {
+                    if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_PRODUCER);
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&kvfull[s], page_bytes * (uint32_t)cur_n);
                 __syncwarp();
-                ++np;
-            }
-            ++segs_p;
-        }
-        // no MMA may still run when tensor memory is released: the last one's barrier
-        if (np > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(&pvdone[(np - 1) & 1u], ((np - 1) >> 1) & 1u, TL_WAIT_LIMIT)) && lane == 0)
-            tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DRAIN);
-        if (nq > np && !__all_sync(0xFFFFFFFFu, mbar_wait(&qkdone[(nq - 1) & 1u], ((nq - 1) >> 1) & 1u, TL_WAIT_LIMIT)) && lane == 0)
-            tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DRAIN);
-    } else if (warp < 4) {
-        // ------------------------------------------------------------ rows
-        constexpr int LPR = D / 8;                 // lanes of a row, 8 channels each
-        constexpr int RPP = 64 / LPR;              // rows of a pass
-        const int t = threadIdx.x - 64;
-        const int c = t % LPR;
-        uint32_t seg = 0;
-        while (walk.next(sg)) {
-            const int n_rows = min((int)rows8[sg.b] * p.group - rt * NT, NT);
-            const int first = p.row_start ? __ldg(p.row_start + sg.b) : sg.b * p.max_rows;
-            if (!__all_sync(0xFFFFFFFFu, tc_wait(qfree, (seg & 1u) ^ 1u, abort_flag))) {
-                if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_PRODUCER);
-                break;
-            }
-#pragma unroll 5
-            for (int n = t / LPR; n < NT; n += RPP) {
-                uint4 q = make_uint4(0, 0, 0, 0);
-                if (n < n_rows) {
-                    const int r = rt * NT + n;
-                    q = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)(first + r / p.group) * p.q_stride +
-                                                             (size_t)(sg.head * p.group + r % p.group) * D) + c);
+                if (lane < cur_n) {
+                    const size_t unit = (size_t)page * p.heads + head;
+                    bulk_load_s(stage0 + (uint32_t)(s * C::STAGE_BYTES) + page_bytes * (uint32_t)lane, p.pages + unit * page_bytes,
+                                page_bytes, &kvfull[s], pol);
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(page_scale + 8 * s + lane)),
+                                 "l"(p.scales + 2 * unit) : "memory");
                 }
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-                unsigned top = 0;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const unsigned lo = w[u] & 0x7FFFu, hi = (w[u] >> 16) & 0x7FFFu;
-                    if (lo < 0x7F80u) top = max(top, lo);
-                    if (hi < 0x7F80u) top = max(top, hi);
-                }
-#pragma unroll
-                for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                const int e = min(max((int)(top >> 7) - 127, -100), 127) - 14;
-                const float f = kv_pow2(-e);
-                uint32_t h[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    h[u] = kv_pack_f16(__int_as_float((int)(w[u] << 16)) * f, __int_as_float((int)(w[u] & 0xFFFF0000u)) * f);
-                *reinterpret_cast<uint4*>(q_sm + (c >> 3) * (NT * 128) + n * 128 + (((c & 7) ^ (n & 7)) << 4)) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
-                if (c == 0) rowf[(seg & 3u) * NT + n] = p.scale * kv_pow2(e);
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&kvfull[s])) : "memory");
+                issued |= 1u << s;
+                last_ph = (last_ph & ~(1u << s)) | (ph << s);
+                if (++s == C::STAGES) { s = 0; ph ^= 1u; }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(qready);
-            ++seg;
+            // every issued copy must land before the CTA can leave
+            for (int i = 0; i < C::STAGES; ++i)
+                if ((issued >> i) & 1u)
+                    if (!mbar_wait(&kvfull[i], (last_ph >> i) & 1u, TL_WAIT_LIMIT >> 4))
+                        if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DRAIN);
+        } else if (warp < 3) {
+            // ------------------------------------------------------------ MMA issuers
+            const uint32_t tmem_u = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            const uint64_t qdesc = kv_uniform64(smem_desc_k_sw128(smem_u32(q_sm)));
+            const uint64_t pdesc = kv_uniform64(smem_desc_mn_sw32(smem_u32(p_sm), C::P_ATOM, C::P_STEP));
+            const bool leader = elect_one();
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (ok && !__all_sync(0xFFFFFFFFu, kv_wait(bar, parity, abort_flag))) {
+                    if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_MMA);
+                    ok = false;
+                }
+            };
+            KvRing<BUFS> ring;
+            uint32_t seg = 0;
+            uint64_t* last_bar = nullptr;
+            uint32_t last_par = 0;
+            while (ok && walk.next(sg)) {
+                for (int k = sg.k0; k < sg.k1; ++k) {
+                    const uint32_t b = ring.i;
+                    if (warp == 1) {
+                        if (k == sg.k0) wait(&qready[seg & 1u], (seg >> 1) & 1u);
+                        wait(&kready[b], ring.par);
+                        wait(&sempty[b], ring.par ^ 1u);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+                            const uint64_t qd = qdesc + (uint64_t)((seg & 1u) * (C::Q_BYTES >> 4));
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i)
+                                mma_ts_f16(tmem_u + (uint32_t)(C::S_COL) + b * NT, tmem_u + (uint32_t)(C::K_COL + 8 * i) + b * C::K_COLS,
+                                           qd + (uint64_t)(((i >> 2) * NT * 128 + (i & 3) * 32) >> 4), C::IDESC, i ? 1u : 0u);
+                            mma_commit(&qkdone[b]);
+                            if (k + 1 == sg.k1) mma_commit(&qfree[seg & 1u]);
+                        }
+                        last_bar = &qkdone[b];
+                    } else {
+                        if (k == sg.k0) wait(oempty, (seg & 1u) ^ 1u);
+                        wait(&vready[b], ring.par);
+                        wait(&pready[b], ring.par);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+                            const uint64_t pd = pdesc + (uint64_t)(b * (C::P_BYTES >> 4));
+#pragma unroll
+                            for (int i = 0; i < KV_TILE / 16; ++i)
+                                mma_ts_f16(tmem_u + (uint32_t)C::O_COL, tmem_u + (uint32_t)(C::V_COL + 8 * i) + b * C::V_COLS,
+                                           pd + (uint64_t)((2 * i * C::P_STEP) >> 4), C::IDESC_P, (i || k != sg.k0) ? 1u : 0u);
+                            mma_commit(&pvdone[b]);
+                            if (k + 1 == sg.k1) mma_commit(ofull);
+                        }
+                        last_bar = &pvdone[b];
+                    }
+                    last_par = ring.par;
+                    __syncwarp();
+                    ring.step();
+                }
+                ++seg;
+            }
+            // no MMA may still run when tensor memory is released: the barrier of this warp's last ones
+            if (last_bar && !__all_sync(0xFFFFFFFFu, mbar_wait(last_bar, last_par, TL_WAIT_LIMIT >> 4)) && lane == 0)
+                tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DRAIN);
+        } else {
+            // ------------------------------------------------------------ rows
+            uint32_t seg = 0;
+            while (walk.next(sg)) {
+                if (seg > 0) {
+                    if (!__all_sync(0xFFFFFFFFu, kv_wait(&qfree[seg & 1u], ((seg >> 1) & 1u) ^ 1u, abort_flag))) {
+                        if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_PRODUCER);
+                        break;
+                    }
+                    kv_load_rows<D, NT, 5>(p, sg, min((int)rows8[sg.b] * p.group - rt * NT, NT), rt * NT, lane, 32,
+                                           q_sm + (seg & 1u) * C::Q_BYTES, rowf + (seg % C::ROWF_RING) * NT);
+                    __syncwarp();
+                    if (lane < 2) mbar_arrive(&qready[seg & 1u]);
+                }
+                ++seg;
+            }
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         // ------------------------------------------------------------ converters
-        const int qd = warp & 3, r = 32 * qd + lane;             // token of the tile; channel
+        regs_dec<C::REGS_CONVERT>();
+        const bool is_v = warp >= 8;
+        const int qd = warp & 3, r = 32 * qd + lane;             // K: token of the tile; V: channel
         const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16);
         const int pl = p.page_log2;
         const uint32_t page_bytes = 2u * D << pl;
-        const uint32_t k_off = (uint32_t)(r >> pl) * page_bytes + (uint32_t)(r & ((1 << pl) - 1)) * 16u, k_step = 16u << pl;
         int s = 0;
         uint32_t ph = 0, n = 0;
+        KvRing<BUFS> ring;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (!__all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort_flag))) {
+            if (!__all_sync(0xFFFFFFFFu, kv_wait(bar, parity, abort_flag))) {
                 if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DEQUANT);
                 ok = false;
             }
         };
         while (ok && walk.next(sg)) {
             for (int k = sg.k0; k < sg.k1; ++k) {
-                const uint32_t b = n & 1u, par = (n >> 1) & 1u;
+                const uint32_t b = ring.i;
                 wait(&kvfull[s], ph);
                 if (!ok) break;
                 const uint8_t* const st = stages + s * C::STAGE_BYTES;
-                uint4 w[8];
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c) w[c] = *reinterpret_cast<const uint4*>(st + k_off + c * k_step);
-                tok[(n & 3u) * KV_TILE + r] = page_scale[8 * s + (r >> pl)];
                 uint32_t out[32];
+                if (!is_v) {
+                    const uint8_t* const at = st + (uint32_t)(r >> pl) * page_bytes + (uint32_t)(r & ((1 << pl) - 1)) * 16u;
+                    uint4 w[8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) kv_decode16(w[c], out + 8 * c);
-                wait(&qkdone[b], par ^ 1u);                       // S^T of the tile two back has read this K tile
-                if (!ok) break;
-                tc_fence_after();
-                tmem_st32(t_lane + (uint32_t)C::K_COL + b * C::K_COLS, out);
-                if (D == 128) {
+                    for (int c = 0; c < D / 16; ++c) w[c] = *reinterpret_cast<const uint4*>(at + ((16u * c) << pl));
+                    const float2 sc = page_scale[8 * s + (r >> pl)];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&kvempty[s]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) kv_decode16(w[4 + c], out + 8 * c);
-                    tmem_st32(t_lane + (uint32_t)C::K_COL + b * C::K_COLS + 32u, out);
-                }
-                if (D == 128 || qd < 2) {
+                    for (int c = 0; c < 4; ++c) kv_decode16(w[c], out + 8 * c);
+                    wait(&qkdone[b], ring.par ^ 1u);              // the S^T that read this K buffer last
+                    if (!ok) break;
+                    tc_fence_after();
+                    // that S^T, of tile n - BUFS, had its buffer from tile n - 2 BUFS, whose scales are thus read: at most
+                    // 2 BUFS tiles' scales are in use
+                    tok[(n % C::TOK_RING) * KV_TILE + r] = sc;
+                    tmem_st32(t_lane + (uint32_t)C::K_COL + b * C::K_COLS, out);
+                    if (D == 128) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) kv_decode16(w[4 + c], out + 8 * c);
+                        tmem_st32(t_lane + (uint32_t)C::K_COL + b * C::K_COLS + 32u, out);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&kready[b]);
+                } else if (D == 128 || qd < 2) {
+                    // tokens behind the request's last one count nothing, whatever their bytes are
+                    const int valid = (k + 1 == sg.tiles) ? last8[sg.b] : KV_TILE;
+                    uint4 w[8];
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         const int t = 16 * c;
                         w[c] = *reinterpret_cast<const uint4*>(st + (uint32_t)(t >> pl) * page_bytes + (uint32_t)(D << pl) +
                                                                (uint32_t)((t & ((1 << pl) - 1)) >> 4) * (16u * D) + 16u * r);
                     }
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) { mbar_arrive(&kvempty[s]); mbar_arrive(&kready[b]); }
-                wait(&pvdone[b], par ^ 1u);                       // O^T of the tile two back has read this V tile
-                if (!ok) break;
-                tc_fence_after();
-                if (D == 128 || qd < 2) {
-                    // tokens behind the request's last one count nothing, whatever their bytes are
-                    const int valid = (k + 1 == sg.tiles) ? last8[sg.b] : KV_TILE;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&kvempty[s]);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -608,43 +681,69 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                                 else if (t + 1 >= valid) out[j] &= 0xFFFFu;
                             }
                         }
+                        if (half == 0) {
+                            wait(&pvdone[b], ring.par ^ 1u);      // the O^T that read this V buffer last
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
                         tmem_st32(t_lane + (uint32_t)C::V_COL + b * C::V_COLS + 32u * half, out);
                     }
+                    if (!ok) break;
                     tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&vready[b]);
+                } else {
+                    // no channels of this quarter: the stage and the buffer pass as they are, in step with the others (an
+                    // arrival ahead of its phase would complete another tile's)
+                    if (lane == 0) mbar_arrive(&kvempty[s]);
+                    wait(&pvdone[b], ring.par ^ 1u);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(&vready[b]);
                 }
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&vready[b]);
                 ++n;
+                ring.step();
                 if (++s == C::STAGES) { s = 0; ph ^= 1u; }
             }
         }
         tmem_wait_st();
     } else {
         // ------------------------------------------------------------ softmax
-        const int grp = (warp - 8) >> 2, qd = warp & 3, t = 32 * qd + lane;      // token of the tile; channel
+        regs_inc<C::REGS_SOFTMAX>();
+        const int grp = (warp - 12) >> 2, qd = warp & 3, t = 32 * qd + lane;     // token of the tile; channel
         const int c0 = grp * NH, bar_id = 1 + grp;
         const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16);
-        const uint32_t p_at = smem_u32(p_sm) + (uint32_t)((t >> 6) * (NT * 128) + (((t & 63) >> 3) << 4) + (t & 7) * 2 + c0 * 128);
+        // this token's rows in P: 16-byte units of 8 rows, two a 32-byte line, swapped in every other four tokens
+        const uint32_t p_line = smem_u32(p_sm) + (uint32_t)((t >> 3) * C::P_STEP + (t & 7) * 32);
+        const uint32_t p_swap = (uint32_t)((t >> 2) & 1) << 4;
         uint32_t n = 0, seg = 0;
+        KvRing<BUFS> ring;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             // a failure is recorded and the warp goes on: the group's barriers need all of its warps
-            if (!__all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort_flag)) && lane == 0)
+            if (!__all_sync(0xFFFFFFFFu, kv_wait(bar, parity, abort_flag)) && lane == 0)
                 tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_EPILOGUE);
         };
         while (walk.next(sg)) {
+            const int n_rows = min((int)rows8[sg.b] * p.group - rt * NT, NT);
+            if (seg == 0) {
+                kv_load_rows<D, NT, 3>(p, sg, n_rows, rt * NT, (int)threadIdx.x - 384, 256, q_sm, rowf);
+                kv_group_sync(bar_id);
+                if (t == 0) mbar_arrive(&qready[0]);
+            }
             float l[NH];
 #pragma unroll
             for (int i = 0; i < NH; ++i) l[i] = 0.0f;
+            uint32_t was_b = 0, was_par = 0;       // the tile before: its buffer
             for (int k = sg.k0; k < sg.k1; ++k) {
-                const uint32_t b = n & 1u, par = (n >> 1) & 1u;
+                const uint32_t b = ring.i;
                 const bool first = k == sg.k0;
-                wait(&qkdone[b], par);
+                wait(&qkdone[b], ring.par);
                 tc_fence_after();
                 float x[NH];
 #pragma unroll
                 for (int i = 0; i < NH; i += 8) tmem_ld8(t_lane + (uint32_t)(C::S_COL + c0 + i) + b * NT, x + i);
-                const float2 sc = tok[(n & 3u) * KV_TILE + t];
+                const float2 sc = tok[(n % C::TOK_RING) * KV_TILE + t];
                 const int valid = (k + 1 == sg.tiles) ? last8[sg.b] : KV_TILE;
                 const bool live = t < valid;
                 const float vs = live ? sc.y : 1.0f;
@@ -658,7 +757,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 float top = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < NH; i += 4) {
-                    const float4 rf = *reinterpret_cast<const float4*>(rowf + (seg & 3u) * NT + c0 + i);
+                    const float4 rf = *reinterpret_cast<const float4*>(rowf + (seg % C::ROWF_RING) * NT + c0 + i);
                     const float4 nm = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *reinterpret_cast<const float4*>(negm + c0 + i);
                     f2_unpack(f2_fma(f2_mul(f2_pack(x[i], x[i + 1]), ks2), f2_pack(rf.x, rf.y), f2_pack(nm.x, nm.y)), x[i], x[i + 1]);
                     f2_unpack(f2_fma(f2_mul(f2_pack(x[i + 2], x[i + 3]), ks2), f2_pack(rf.z, rf.w), f2_pack(nm.z, nm.w)), x[i + 2], x[i + 3]);
@@ -692,7 +791,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                         negm[c0 + t] = -now;
                     }
                     kv_group_sync(bar_id);
-                    if (!first) wait(&pvdone[b ^ 1u], ((n - 1) >> 1) & 1u);     // O holds every tile before this one
+                    if (!first) wait(&pvdone[was_b], was_par);    // O holds every tile before this one
                     tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < NH; i += 8) {
@@ -716,39 +815,53 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                         for (int i = 0; i < NH; ++i) x[i] = live ? x[i] : -INFINITY;
                     }
                 }
-                wait(&pvdone[b], par ^ 1u);                       // P's buffer: O^T of the tile two back has read it
+                wait(&pvdone[b], ring.par ^ 1u);                  // the O^T that read this P buffer last
                 const float vs8 = vs * 256.0f;                    // 2^KV_P_SHIFT
                 const uint64_t vs2 = f2_pack(vs8, vs8);
-                const uint32_t at = p_at + b * C::P_BYTES;
+                const uint32_t at = p_line + b * C::P_BYTES;
 #pragma unroll
-                for (int i = 0; i < NH; i += 2) {
-                    const uint64_t e2 = f2_pack(kv_ex2(x[i]), kv_ex2(x[i + 1]));
-                    f2_unpack(f2_add(f2_pack(l[i], l[i + 1]), e2), l[i], l[i + 1]);
-                    float w0, w1;
-                    f2_unpack(f2_mul(e2, vs2), w0, w1);
-                    const uint32_t h = kv_pack_f16(w0, w1);
-                    sts_u16((at ^ (uint32_t)((i & 7) << 4)) + (uint32_t)(i * 128), h);
-                    sts_u16((at ^ (uint32_t)(((i + 1) & 7) << 4)) + (uint32_t)((i + 1) * 128), h >> 16);
+                for (int i = 0; i < NH; i += 8) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const uint64_t e2 = f2_pack(kv_ex2(x[i + j]), kv_ex2(x[i + j + 1]));
+                        f2_unpack(f2_add(f2_pack(l[i + j], l[i + j + 1]), e2), l[i + j], l[i + j + 1]);
+                        float w0, w1;
+                        f2_unpack(f2_mul(e2, vs2), w0, w1);
+                        h[j >> 1] = kv_pack_f16(w0, w1);
+                    }
+                    const uint32_t u = (uint32_t)(c0 + i) >> 3;   // unit of 8 rows
+                    sts_128(at + (u >> 1) * C::P_ATOM + (((u & 1u) << 4) ^ p_swap), h[0], h[1], h[2], h[3]);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pready[b]);
+                was_b = b;
+                was_par = ring.par;
                 ++n;
+                ring.step();
             }
-            // the segment's part: l over the lanes and warps, O as it lies
+            // the segment's part: l over the lanes (eight rows at a time: three exchanges leave a lane one row) and
+            // warps, O as it lies
 #pragma unroll
-            for (int i = 0; i < NH; ++i) {
-                float v = l[i];
+            for (int i = 0; i < NH; i += 8) {
+                float v[8];
 #pragma unroll
-                for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-                l[i] = v;
+                for (int j = 0; j < 8; ++j) v[j] = l[i + j];
+#pragma unroll
+                for (int w = 4, d = 1; w; w >>= 1, d <<= 1) {
+#pragma unroll
+                    for (int j = 0; j < w; ++j) {
+                        const bool hi = lane & d;
+                        const float mine = hi ? v[j + w] : v[j], other = hi ? v[j] : v[j + w];
+                        v[j] = mine + __shfl_xor_sync(0xFFFFFFFFu, other, d);
+                    }
+                }
+                v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 8);
+                v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);
+                if (lane < 8) red[(grp * 4 + qd) * NH + i + ((lane & 1) << 2) + (lane & 2) + (lane >> 2)] = v[0];
             }
-            if (lane == 0) {
-#pragma unroll
-                for (int i = 0; i < NH; ++i) red[(grp * 4 + qd) * NH + i] = l[i];
-            }
-            const int n_rows = min((int)rows8[sg.b] * p.group - rt * NT, NT);
             const size_t slot = (((size_t)sg.b * p.heads + sg.head + g) * p.row_tiles + rt) * NT;
             kv_group_sync(bar_id);
             if (t < NH && c0 + t < n_rows) {
@@ -868,6 +981,7 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
     }
     // the parts of the cached tokens
     const int len = kv_len_of(p, b);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!mine) return;
     if (len > 0) {
         const int tiles = kv_tiles(len);
@@ -875,20 +989,29 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
         const long long a = (long long)p.heads * before + (long long)head * tiles, z = a + tiles;
         const int g0 = (int)(((a + 1) * groups - 1) / total), g1 = (int)((z * groups - 1) / total);
         const int r = i * p.group + h % p.group, rt = r / p.nt, n = r % p.nt;
-        for (int g = g0; g <= g1; ++g) {
-            const size_t at = (((size_t)b * p.heads + head + g) * p.row_tiles + rt) * p.nt + n;
-            const float2 ml = __ldcg(p.part_ml + at);
-            const float top = fmaxf(m, ml.x);
-            // a part or tree without weight (m of minus infinity) counts nothing
-            const float f0 = (m == -INFINITY) ? 0.0f : exp2f(m - top), f1 = (ml.x == -INFINITY) ? 0.0f : exp2f(ml.x - top);
-            m = top;
-            l = l * f0 + ml.y * f1;
-            const float* const po = p.part_o + at * D + E * lane;
+        // four parts' loads in flight at once
+        for (int g = g0; g <= g1; g += 4) {
+            float2 ml[4], x[4][E / 2];
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(po + e));
-                o[e] = o[e] * f0 + x.x * f1;
-                o[e + 1] = o[e + 1] * f0 + x.y * f1;
+            for (int u = 0; u < 4; ++u) {
+                const size_t at = (((size_t)b * p.heads + head + min(g + u, g1)) * p.row_tiles + rt) * p.nt + n;
+                ml[u] = (g + u <= g1) ? __ldcg(p.part_ml + at) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                for (int e = 0; e < E; e += 2) x[u][e / 2] = __ldcg(reinterpret_cast<const float2*>(p.part_o + at * D + E * lane + e));
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (g + u > g1) break;
+                const float top = fmaxf(m, ml[u].x);
+                // a part or tree without weight (m of minus infinity) counts nothing
+                const float f0 = (m == -INFINITY) ? 0.0f : exp2f(m - top), f1 = (ml[u].x == -INFINITY) ? 0.0f : exp2f(ml[u].x - top);
+                m = top;
+                l = l * f0 + ml[u].y * f1;
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    o[e] = o[e] * f0 + x[u][e / 2].x * f1;
+                    o[e + 1] = o[e + 1] * f0 + x[u][e / 2].y * f1;
+                }
             }
         }
     }

@@ -1315,8 +1315,18 @@ tl_status launch_kv_attention(const tl::KvAttnParams& p, cudaStream_t stream) {
     if (st != TL_OK) return st;
     const int warps = tl::KV_MERGE_THREADS / 32;
     const dim3 grid((unsigned)p.B, (unsigned)((p.max_rows * p.heads * p.group + warps - 1) / warps));
-    tl::kv_merge_kernel<D><<<grid, tl::KV_MERGE_THREADS, 0, stream>>>(p);
-    TL_CUDA(cudaGetLastError());
+    // brought up while the streaming kernel runs: it works on the tree's own rows, then waits for the parts
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(tl::KV_MERGE_THREADS);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    TL_CUDA(cudaLaunchKernelEx(&cfg, tl::kv_merge_kernel<D>, p));
     return TL_OK;
 }
 

@@ -330,6 +330,18 @@ def test_attention_ragged_batch(D):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("D,hq,hkv,rows", [(64, 16, 4, 16), (128, 10, 2, 32), (64, 2, 2, 1)])
+def test_attention_many_tiles_and_requests_a_block(D, hq, hkv, rows):
+    # every block walks over several requests and heads, and over several tiles of most of them
+    rs = np.random.default_rng(D + rows)
+    n = 12
+    c = Case(6, [int(x) for x in rs.integers(0, 3000, n)], [int(x) for x in rs.integers(1, rows + 1, n)], hq, hkv, D, 16).device()
+    y = c.run()
+    c.check(y)
+    for _ in range(5):
+        assert torch.equal(y, c.run())
+
+
 def test_attention_long_context_and_many_requests():
     c = Case(8, [9000], [4], 5, 1, 128, 64).device()
     c.check(c.run())
