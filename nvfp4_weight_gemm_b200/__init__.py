@@ -216,26 +216,48 @@ def gdn_commit(state, k, v, alpha, beta, path, stream=None):
 
 
 # ---------------------------------------------------------------- 8-bit paged KV cache
+#
+# What the library cannot see behind a pointer (types, shapes, devices) is checked here, with few Python
+# operations: these calls come every decoding round.
 
-def _expect(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _refuse(what: str):
+    raise ValueError(what)
 
 
-def _ints(name, t, shape, device):
+def _ints(name, t, shape, index):
+    """Pointer of a contiguous int32 tensor of `shape` on CUDA device `index`."""
     import torch
-    _expect(t.dtype == torch.int32 and tuple(t.shape) == tuple(shape) and t.is_contiguous() and t.device == device,
-            f"{name}: need a contiguous int32 tensor of shape {tuple(shape)} on {device}, "
-            f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(f"{name}: need a contiguous int32 tensor of shape {tuple(shape)} on cuda:{index}, "
+                f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _rows(name, t, heads, dim, device):
-    """The row stride of bf16 rows [n, heads, dim] whose heads lie side by side (any distance between rows)."""
+def _rows(name, t, heads, dim, index):
+    """(rows, distance between rows) of bf16 rows [n, heads, dim] whose heads lie side by side."""
     import torch
-    _expect(t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[1] == heads and t.shape[2] == dim and t.device == device,
-            f"{name}: need bf16 [rows, {heads}, {dim}] on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    _expect(t.stride(2) == 1 and (heads == 1 or t.stride(1) == dim), f"{name}: the heads of a row must lie side by side")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0) // 8 * 8, heads * dim)
+    n, h, d = t.shape if t.dim() == 3 else (0, -1, -1)
+    if h != heads or d != dim or t.dtype is not torch.bfloat16 or t.get_device() != index:
+        _refuse(f"{name}: need bf16 [rows, {heads}, {dim}] on cuda:{index}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    a, b, c = t.stride()
+    if c != 1 or (b != dim and heads > 1):
+        _refuse(f"{name}: the heads of a row must lie side by side")
+    return n, (a if n > 1 else heads * dim)
+
+
+def _stream_of(index, stream):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _call_on(index, fn, *args):
+    """fn(*args) with CUDA device `index` current."""
+    import torch
+    if torch._C._cuda_getDevice() == index:
+        check(fn(*args))
+    else:
+        with torch.cuda.device(index):
+            check(fn(*args))
 
 
 class KvCache:
@@ -243,15 +265,21 @@ class KvCache:
     [dim/16, tokens, 16], V as [tokens/16, dim, 16]) and `scales` float32 [n_pages, kv_heads, 2] (powers of two).
     Holds the two tensors; kv_commit() fills them, kv_attention() reads them."""
 
+    __slots__ = ("pages", "scales", "page_tokens", "n_pages", "kv_heads", "head_dim", "index", "_c")
+
     def __init__(self, pages, scales, page_tokens: int):
         import torch
-        _expect(pages.dtype == torch.uint8 and pages.dim() == 4 and pages.shape[2] == 2 and pages.is_contiguous(),
-                "pages: need a contiguous uint8 tensor [n_pages, kv_heads, 2, page_tokens * head_dim]")
-        _expect(page_tokens > 0 and pages.shape[3] % page_tokens == 0, "pages: page_tokens does not divide a page's side")
-        _expect(scales.dtype == torch.float32 and tuple(scales.shape) == tuple(pages.shape[:3]) and scales.is_contiguous()
-                and scales.device == pages.device, "scales: need a contiguous float32 tensor [n_pages, kv_heads, 2] beside pages")
-        self.pages, self.scales, self.page_tokens = pages, scales, int(page_tokens)
-        self.n_pages, self.kv_heads, self.head_dim = pages.shape[0], pages.shape[1], pages.shape[3] // int(page_tokens)
+        shape = pages.shape
+        if pages.dtype is not torch.uint8 or len(shape) != 4 or shape[2] != 2 or not pages.is_contiguous():
+            _refuse("pages: need a contiguous uint8 tensor [n_pages, kv_heads, 2, page_tokens * head_dim]")
+        n, heads, _, side = shape
+        if page_tokens <= 0 or side % page_tokens:
+            _refuse("pages: page_tokens does not divide a page's side")
+        if scales.dtype is not torch.float32 or scales.shape != shape[:3] or not scales.is_contiguous() or scales.device != pages.device:
+            _refuse("scales: need a contiguous float32 tensor [n_pages, kv_heads, 2] beside pages")
+        self.pages, self.scales, self.page_tokens = pages, scales, page_tokens
+        self.n_pages, self.kv_heads, self.head_dim, self.index = n, heads, side // page_tokens, pages.get_device()
+        self._c = _lib.KvCacheC(pages.data_ptr(), scales.data_ptr(), n, page_tokens, heads, self.head_dim)
 
     @classmethod
     def empty(cls, n_pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
@@ -260,17 +288,8 @@ class KvCache:
         return cls(torch.empty((n_pages, kv_heads, 2, page_tokens * head_dim), dtype=torch.uint8, device=device),
                    torch.empty((n_pages, kv_heads, 2), dtype=torch.float32, device=device), page_tokens)
 
-    def _c(self):
-        return _lib.KvCacheC(self.pages.data_ptr(), self.scales.data_ptr(), self.n_pages, self.page_tokens, self.kv_heads,
-                             self.head_dim)
-
-
-def _on(device, stream):
-    """(device guard, stream pointer): the given stream, or the device's current one."""
-    import torch
-    _expect(device.type == "cuda", f"tensors must be on a CUDA device, got {device}")
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return torch.cuda.device(device), ctypes.c_void_p(s.cuda_stream)
+    def _on_gpu(self):
+        return self.index if self.index >= 0 else _refuse("the cache must be on a CUDA device")
 
 
 def kv_slots(lens, want, table, free_pages, n_free, page_tokens, slots, starts, info, stream=None):
@@ -281,16 +300,14 @@ def kv_slots(lens, want, table, free_pages, n_free, page_tokens, slots, starts, 
     slots [max_slots] (a slot for every token that requests grow by, then -1), starts [B + 1], info [4]
     (code, pages missing, slots missing, requests refused). lens, table, free_pages and n_free are updated in place.
     Returns (slots, starts, info)."""
-    dev = lens.device
-    B = lens.shape[0] if lens.dim() == 1 else -1
-    for name, t, shape in (("lens", lens, (B,)), ("want", want, (B,)), ("n_free", n_free, (1,)), ("starts", starts, (B + 1,)),
-                           ("info", info, (4,)), ("slots", slots, (slots.numel(),)), ("free_pages", free_pages, (free_pages.numel(),)),
-                           ("table", table, (B, table.shape[-1]))):
-        _ints(name, t, shape, dev)
-    guard, st = _on(dev, stream)
-    with guard:
-        check(_lib.lib().tl_kv_slots(_ptr(lens), _ptr(want), B, page_tokens, _ptr(table), table.shape[1], _ptr(free_pages),
-                                     free_pages.numel(), _ptr(n_free), _ptr(slots), slots.numel(), _ptr(starts), _ptr(info), st))
+    index = lens.get_device()
+    if index < 0 or lens.dim() != 1:
+        _refuse("lens: need an int32 tensor [B] on a CUDA device")
+    B, width, n_pages, room = lens.shape[0], table.shape[-1], free_pages.numel(), slots.numel()
+    _call_on(index, _lib.lib().tl_kv_slots, _ints("lens", lens, (B,), index), _ints("want", want, (B,), index), B, page_tokens,
+             _ints("table", table, (B, width), index), width, _ints("free_pages", free_pages, (n_pages,), index), n_pages,
+             _ints("n_free", n_free, (1,), index), _ints("slots", slots, (room,), index), room,
+             _ints("starts", starts, (B + 1,), index), _ints("info", info, (4,), index), _stream_of(index, stream))
     return slots, starts, info
 
 
@@ -299,26 +316,20 @@ def kv_commit(cache, k, v, slots, src=None, stream=None):
 
     k, v bf16 [rows, kv_heads, head_dim] (rows may be slices of the QKV projection's output); slots int32 [n] as
     kv_slots() writes them (negative: nowhere); src int32 [n] or None. Returns `cache`."""
-    dev = cache.pages.device
+    index = cache._on_gpu()
+    rows = _rows("k", k, cache.kv_heads, cache.head_dim, index)
+    if _rows("v", v, cache.kv_heads, cache.head_dim, index) != rows:
+        _refuse("k and v must have the same rows and row stride")
     n = slots.numel()
-    stride = _rows("k", k, cache.kv_heads, cache.head_dim, dev)
-    _expect(_rows("v", v, cache.kv_heads, cache.head_dim, dev) == stride and v.shape == k.shape,
-            "k and v must have the same shape and row stride")
-    _ints("slots", slots, (n,), dev)
-    if src is not None:
-        _ints("src", src, (n,), dev)
-    c = cache._c()
-    guard, st = _on(dev, stream)
-    with guard:
-        check(_lib.lib().tl_kv_commit(ctypes.byref(c), _ptr(k), _ptr(v), stride, k.shape[0],
-                                      _ptr(src) if src is not None else None, _ptr(slots), n, st))
+    _call_on(index, _lib.lib().tl_kv_commit, cache._c, k.data_ptr(), v.data_ptr(), rows[1], rows[0],
+             None if src is None else _ints("src", src, (n,), index), _ints("slots", slots, (n,), index), n, _stream_of(index, stream))
     return cache
 
 
 def kv_attention_workspace(cache, n_q_heads: int, batch: int, max_rows: int) -> int:
     """Bytes of workspace kv_attention() needs for these sizes."""
-    c, n = cache._c(), ctypes.c_size_t()
-    check(_lib.lib().tl_kv_attention_workspace(ctypes.byref(c), n_q_heads, batch, max_rows, ctypes.byref(n)))
+    n = ctypes.c_size_t()
+    check(_lib.lib().tl_kv_attention_workspace(cache._c, n_q_heads, batch, max_rows, ctypes.byref(n)))
     return n.value
 
 
@@ -333,45 +344,47 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
     (None: R / B rows each). scale defaults to head_dim ** -0.5. out bf16 [R, q_heads, head_dim]; workspace uint8 of
     kv_attention_workspace() bytes (both allocated when None). Returns `out`."""
     import torch
-    dev = cache.pages.device
-    R, hq = q.shape[0], q.shape[1]
-    B = lens.shape[0]
-    q_stride = _rows("q", q, hq, cache.head_dim, dev)
-    _ints("lens", lens, (B,), dev)
-    _ints("table", table, (B, table.shape[-1]), dev)
+    index, heads, dim = cache._on_gpu(), cache.kv_heads, cache.head_dim
+    hq = q.shape[1] if q.dim() == 3 else -1
+    R, q_stride = _rows("q", q, hq, dim, index)
+    B, width = lens.numel(), table.shape[-1]
     if row_start is not None:
-        _ints("row_start", row_start, (B + 1,), dev)
-        _expect(max_rows is not None, "row_start needs max_rows, the most rows of one request")
+        if max_rows is None:
+            _refuse("row_start needs max_rows, the most rows of one request")
     elif max_rows is None:
-        _expect(B > 0 and R % B == 0, f"{R} rows do not go round {B} requests: give row_start")
-        max_rows = R // B
-    if mask is not None:
-        _ints("mask", mask, (R,), dev)
-    new_stride = 0
-    _expect((k_new is None) == (v_new is None), "k_new and v_new go together")
-    if k_new is not None:
-        new_stride = _rows("k_new", k_new, cache.kv_heads, cache.head_dim, dev)
-        _expect(k_new.shape[0] == R and v_new.shape == k_new.shape and
-                _rows("v_new", v_new, cache.kv_heads, cache.head_dim, dev) == new_stride,
-                "k_new and v_new must have q's rows and one row stride")
-    if out is None:
-        out = torch.empty((R, hq, cache.head_dim), dtype=torch.bfloat16, device=dev)
-    out_stride = _rows("out", out, hq, cache.head_dim, dev)
-    _expect(out.shape[0] == R, "out must have q's rows")
+        max_rows = R // B if B and R % B == 0 else _refuse(f"{R} rows do not go round {B} requests: give row_start")
+    new_stride, k_ptr, v_ptr = 0, None, None
+    if k_new is not None or v_new is not None:
+        if k_new is None or v_new is None:
+            _refuse("k_new and v_new go together")
+        new = _rows("k_new", k_new, heads, dim, index)
+        if new[0] != R or _rows("v_new", v_new, heads, dim, index) != new:
+            _refuse("k_new and v_new must have q's rows and one row stride")
+        new_stride, k_ptr, v_ptr = new[1], k_new.data_ptr(), v_new.data_ptr()
+    made = out is None
+    if made:
+        out = torch.empty((R, hq, dim), dtype=torch.bfloat16, device=q.device)
+        out_stride = hq * dim
+    else:
+        n, out_stride = _rows("out", out, hq, dim, index)
+        if n != R:
+            _refuse("out must have q's rows")
     if R == 0:
         return out
-    c = cache._c()
-    guard, st = _on(dev, stream)
-    with guard:
-        if workspace is None:
-            workspace = torch.empty(kv_attention_workspace(cache, hq, B, max_rows), dtype=torch.uint8, device=dev)
-            if stream is not None:
-                workspace.record_stream(stream)
-                out.record_stream(stream)
-        check(_lib.lib().tl_kv_attention(
-            _ptr(q), q_stride, hq, ctypes.byref(c), _ptr(table), table.shape[1], _ptr(lens), B,
-            _ptr(k_new) if k_new is not None else None, _ptr(v_new) if v_new is not None else None, new_stride,
-            _ptr(mask) if mask is not None else None, _ptr(row_start) if row_start is not None else None, R, max_rows,
-            float(cache.head_dim ** -0.5 if scale is None else scale), _ptr(out), out_stride, _ptr(workspace),
-            workspace.numel(), st))
+    own_workspace = workspace is None
+    if own_workspace:
+        workspace = torch.empty(kv_attention_workspace(cache, hq, B, max_rows), dtype=torch.uint8, device=q.device)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+        _refuse(f"workspace: need a contiguous uint8 tensor on cuda:{index}")
+    _call_on(index, _lib.lib().tl_kv_attention, q.data_ptr(), q_stride, hq, cache._c, _ints("table", table, (B, width), index), width,
+             _ints("lens", lens, (B,), index), B, k_ptr, v_ptr, new_stride,
+             None if mask is None else _ints("mask", mask, (R,), index),
+             None if row_start is None else _ints("row_start", row_start, (B + 1,), index), R, max_rows,
+             dim ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, workspace.data_ptr(), workspace.numel(),
+             _stream_of(index, stream))
+    if stream is not None:   # what was allocated here for another stream than the current one
+        if made:
+            out.record_stream(stream)
+        if own_workspace:
+            workspace.record_stream(stream)
     return out

@@ -130,27 +130,30 @@ struct KvSegIter {
 // Both products run on the tensor cores with the cache as operand A and the rows as operand B, so that
 // few rows cost little (an MMA is 128 tokens or channels times NT rows, NT a multiple of 16):
 //
-//     S^T [token][row]   = K  [token][channel] . Q^T      A = K in tensor memory,  B = Q in shared memory
-//     O^T [channel][row] = V^T [channel][token] . P^T     A = V in tensor memory,  B = P in shared memory
+//     S^T [token][row]   = K  [token][channel] . Q^T      E4M3: A = the cache's bytes in shared memory as they are
+//     O^T [channel][row] = V^T [channel][token] . P^T     f16:  A = V in tensor memory,  B = P in shared memory
 //
-// K and V become f16 on the way (every E4M3 value is an f16 value). Q rows become f16 after an exact
-// scaling of each by a power of two that brings its largest magnitude into [2^14, 2^15): a bf16 value has 8
-// significant bits, so every element within 2^-24 of that is exact and the others are within 2^-40 of it. P is
-// rounded to f16 (11 bits against the output's 8) after a scaling that leaves 2^-22 of the largest
-// weight normal; the sums l take p before that rounding. S, O and l are fp32.
+// K is never converted: Q is. Each row of Q is scaled by a power of two that brings its largest magnitude into
+// (224, 448] and written as the sum of two E4M3 terms, the second holding what the first left over. A bf16 value
+// has 8 significant bits and a term holds 4, so the sum is exact for elements down to 2^-10 of the largest; the
+// others are within 2^-10 in that scale, 2^-17.8 of the row's largest. Both terms multiply the same K into one fp32
+// accumulator (products of E4M3 are exact in it).
+// P would lose too much in E4M3: it keeps f16 (11 bits against the output's 8), after a scaling that leaves 2^-22 of
+// the largest weight normal, and V becomes f16 on the way (every E4M3 value is an f16 value). The sums l take
+// p before that rounding. S, O and l are fp32.
 //
 // The reference m of a row's weights is kept as long as no log-weight of a tile passes it by more than
 // KV_SLACK; only then (and in a segment's first tile) are the tile's maxima found across lanes, and O and
 // l rescaled. So most tiles need one comparison a score and one vote.
 //
 // Roles (one CTA of 20 warps per SM; registers are moved between the warpgroups, KvCfg):
-//   * warp 0        producer: a page's K and V of the head are one contiguous piece, brought in by one bulk copy;
-//                   tiles of 128 tokens, a ring of stages. Scales follow by cp.async.
+//   * warp 0        producer: bulk copies of a tile's pages (128 tokens) into a ring of stages: K in pieces of 16
+//                   channels, so that a tile of several pages is one operand, V a piece a page. Scales follow by cp.async.
 //   * warp 1        issues the MMAs of S^T, warp 2 those of O^T (an issuer manages one MMA in some 55 cycles while
 //                   other warps run, so one warp for all sixteen of a tile was a bound).
-//   * warp 3        the rows: Q of the next segment, scaled, to one of two buffers in shared memory. The first
-//                   segment's Q is brought in by the softmax warps, which have nothing to do yet.
-//   * warps 4..7    K converters, lane = token; warps 8..11 V converters, lane = channel; 16 bytes of a lane at a time.
+//   * warp 3        the rows: Q of the next segment to one of two buffers in shared memory. The first segment's Q is
+//                   brought in by the softmax warps, which have nothing to do yet.
+//   * warps 4..11   V converters, two sets of four that take turns; lane = channel, 16 bytes of a lane at a time.
 //   * warps 12..19  softmax: two groups of four warps, half of the rows each, lane = token. A group also reads its
 //                   rows of O (lane = channel) when a segment ends and writes the part.
 // Every mbarrier wait is bounded; after one has run out the others return at once, every role runs to its end
@@ -166,35 +169,37 @@ struct KvCfg {
     static constexpr int REGS_CONTROL = 64, REGS_CONVERT = 80, REGS_SOFTMAX = 128;
     static_assert(REGS_CONTROL + 2 * REGS_CONVERT + 2 * REGS_SOFTMAX <= 480, "registers of the launch");
     static constexpr int NH = NT / 2;                          // rows of a softmax group
-    static constexpr int STAGE_BYTES = 2 * KV_TILE * D;
-    static constexpr int Q_BYTES = NT * D * 2;                 // D/64 slabs of [NT][64] f16, 128-byte rows, swizzled
-    static constexpr int P_BYTES = NT * KV_TILE * 2;           // two slabs of [NT][64 tokens]
+    static constexpr int SIDE_BYTES = KV_TILE * D;             // K of a tile: [D/16][128][16]; V: [8][D][16]
+    static constexpr int STAGE_BYTES = 2 * SIDE_BYTES;
+    static constexpr int QSTEPS = 2 * D / 32;                  // MMAs of S^T: 32 channels each, both terms
+    static constexpr int Q_BYTES = NT * D * 2;                 // slabs of [NT] 128-byte rows, swizzled: the first terms, the second
+    static constexpr int P_BYTES = NT * KV_TILE * 2;
+    // tiles in flight between converters, MMAs and softmax: what tensor memory (and for 80 rows shared memory) holds
+    static constexpr int BUFS = (4 * (KV_TILE / 2 + NT) + NT <= 512) ? 4 : (NT <= 64) ? 3 : 2;
     static constexpr int PRE_INTS = KV_MAX_BATCH + 4;
     // S^T runs up to BUFS tiles (so perhaps BUFS segments) ahead of the softmax, and Q two segments ahead of S^T
-    static constexpr int TOK_RING = 8, ROWF_RING = 8;
+    static constexpr int ROWF_RING = 8;
+    // page scales: the producer is up to STAGES tiles ahead of S^T, and that BUFS ahead of the softmax
+    static constexpr int SCALE_RING = 16;
     static constexpr int SMALL_BYTES = PRE_INTS * 4 + 2 * KV_MAX_BATCH    // tiles in front, rows, last tile's tokens
-                                     + TOK_RING * KV_TILE * 8             // token scales
+                                     + SCALE_RING * 8 * 8                 // page scales
                                      + ROWF_RING * NT * 4                 // row factors
                                      + 3 * NT * 4                         // -m, rescaling factors, sums
                                      + 2 * 4 * NH * 4                     // a group's four warps' maxima or sums
-                                     + 8 * 8 * 8                          // page scales of the stages
                                      + 512;                               // barriers
-    // tiles in flight between converters, MMAs and softmax: three where tensor memory holds them
-    static constexpr int BUFS = (3 * (D / 2 + KV_TILE / 2 + NT) + NT <= 512) ? 3 : 2;
-    static_assert(TOK_RING >= 2 * BUFS && ROWF_RING >= BUFS + 3, "rings");
     static constexpr int FIXED = 2 * Q_BYTES + BUFS * P_BYTES + SMALL_BYTES + 1024 /*align*/;
     static constexpr int FIT = (232448 - FIXED) / STAGE_BYTES;
-    static constexpr int STAGES = FIT < 6 ? FIT : 6;
+    static constexpr int STAGES = FIT < 8 ? FIT : 8;
+    static_assert(ROWF_RING >= BUFS + 3 && SCALE_RING >= STAGES + BUFS, "rings");
     static constexpr int SMEM_BYTES = FIXED + STAGES * STAGE_BYTES;
-    static constexpr uint32_t IDESC = idesc_f16(0u /*f16*/, 128u, (uint32_t)NT);
-    static constexpr uint32_t IDESC_P = IDESC | (1u << 16);    // B = P: rows fastest
+    static constexpr uint32_t IDESC_QK = (1u << 4) /*fp32*/ | ((uint32_t)(NT >> 3) << 17) | ((128u >> 4) << 24);   // E4M3 x E4M3
+    static constexpr uint32_t IDESC_PV = idesc_f16(0u /*f16*/, 128u, (uint32_t)NT) | (1u << 16);                   // B: rows fastest
     // P lies token by token, rows fastest (a softmax thread holds one token's rows): atoms of 8 tokens x 16 rows,
     // 32 bytes a token, 32-byte swizzle; the atoms of 8 tokens side by side, then the next 8 tokens
     static constexpr int P_ATOM = 256, P_STEP = (NT / 16) * P_ATOM;
-    // tensor memory columns: K tiles, V tiles, S^T, one O^T
-    static constexpr int K_COL = 0, K_COLS = D / 2;
-    static constexpr int V_COL = BUFS * K_COLS, V_COLS = KV_TILE / 2;
-    static constexpr int S_COL = V_COL + BUFS * V_COLS;
+    // tensor memory columns: V tiles, S^T, one O^T
+    static constexpr int V_COL = 0, V_COLS = KV_TILE / 2;
+    static constexpr int S_COL = BUFS * V_COLS;
     static constexpr int O_COL = S_COL + BUFS * NT;
     static constexpr int TMEM_COLS = 512;
     static_assert(O_COL + NT <= TMEM_COLS, "tensor memory budget");
@@ -299,9 +304,24 @@ __device__ __forceinline__ void kv_decode16(uint4 q, uint32_t* out) {
 __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
     for (uint32_t i = 0; i < (TL_WAIT_LIMIT >> 4); ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
+        if ((i & 15u) == 15u && *abort_flag) return false;
     }
     return false;
+}
+
+// Shared-memory matrix descriptor of a K-major operand without swizzle: 16-byte rows, 8 of them 128 contiguous bytes,
+// `rows8` bytes from one group of 8 rows to the next, `k16` bytes from one 16-byte step along the summed axis to the next.
+__device__ __forceinline__ uint64_t smem_desc_k_plain(uint32_t saddr, uint32_t rows8, uint32_t k16) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(k16 >> 4) << 16) | ((uint64_t)(rows8 >> 4) << 32) | ((uint64_t)1u << 46);
+}
+
+// D[tmem] (+)= A[smem] * B[smem], E4M3 operands, fp32 accumulate.
+__device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
 __device__ __forceinline__ uint64_t kv_uniform64(uint64_t v) {
@@ -331,9 +351,10 @@ struct KvRing {
     }
 };
 
-// The Q rows of a segment's row tile into shared memory as f16, each scaled by a power of two (two K-major slabs of
-// 64 channels, 128-byte swizzle); rowf[n] undoes the scale. By `threads` threads (a multiple of 32), in batches of
-// loads that are all in flight at once.
+// The Q rows of a segment's row tile into shared memory as two E4M3 terms, each row scaled by a power of two; rowf[n]
+// undoes the scale. D = 128: a slab of 128-byte rows for each term; D = 64: one slab, both terms side by side (128-byte
+// swizzle). A non-finite element becomes NaN, and so does its row. By `threads` threads (a multiple of 32), in batches
+// of loads that are all in flight at once.
 template <int D, int NT, int BATCH>
 __device__ __forceinline__ void kv_load_rows(const KvAttnParams& p, const KvSeg& sg, int n_rows, int r0, int t, int threads, uint8_t* q_sm,
                                              float* rowf) {
@@ -367,14 +388,23 @@ __device__ __forceinline__ void kv_load_rows(const KvAttnParams& p, const KvSeg&
 #pragma unroll
             for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
             if (n < NT) {
-                const int e = min(max((int)(top >> 7) - 127, -100), 127) - 14;
+                // the smallest e with top <= 448 * 2^e: the significand's 7 bits behind the point against 1.75
+                const int e = max((int)(top >> 7) - 127, -100) - 8 + ((top & 0x7Fu) > 0x60u);
                 const float f = kv_pow2(-e);
-                uint32_t h[4];
+                uint32_t hi[2], lo[2];
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    h[v] = kv_pack_f16(__int_as_float((int)(w[v] << 16)) * f, __int_as_float((int)(w[v] & 0xFFFF0000u)) * f);
-                *reinterpret_cast<uint4*>(q_sm + (c >> 3) * (NT * 128) + n * 128 + (((c & 7) ^ (n & 7)) << 4)) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
+                for (int v = 0; v < 4; ++v) {
+                    const float x = kv_scaled(w[v] & 0xFFFFu, f), y = kv_scaled(w[v] >> 16, f);
+                    const uint32_t a = kv_e4m3x2(x, y), h = kv_f16x2(a);
+                    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                    const uint32_t b = kv_e4m3x2(x - back.x, y - back.y);
+                    hi[v >> 1] = (v & 1) ? (hi[v >> 1] | (a << 16)) : a;
+                    lo[v >> 1] = (v & 1) ? (lo[v >> 1] | (b << 16)) : b;
+                }
+                uint8_t* const row = q_sm + n * 128;
+                const int c2 = (D == 128) ? c : c + 8, slab2 = (D == 128) ? NT * 128 : 0;
+                *reinterpret_cast<uint2*>(row + (((c >> 1) ^ (n & 7)) << 4) + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(row + slab2 + (((c2 >> 1) ^ (n & 7)) << 4) + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
                 if (c == 0) rowf[n] = p.scale * kv_pow2(e);
             }
         }
@@ -394,23 +424,21 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     uint8_t* const stages = p_sm + BUFS * C::P_BYTES;
     uint64_t* const bars = reinterpret_cast<uint64_t*>(stages + C::STAGES * C::STAGE_BYTES);
     uint64_t* const kvfull = bars;               // [8] a stage's bytes and scales landed
-    uint64_t* const kvempty = kvfull + 8;        // [8] read by the converters
-    uint64_t* const kready = kvempty + 8;        // [3] K tile in tensor memory
-    uint64_t* const qkdone = kready + 3;         // [3] S^T complete (and the K tile free)
-    uint64_t* const sempty = qkdone + 3;         // [3] S^T read by the softmax warps
-    uint64_t* const vready = sempty + 3;         // [3] V tile in tensor memory
-    uint64_t* const pready = vready + 3;         // [3] P in shared memory, O rescaled if need be
-    uint64_t* const pvdone = pready + 3;         // [3] O^T has the tile (and the V tile and P are free)
-    uint64_t* const qready = pvdone + 3;         // [2] Q of a segment in shared memory
+    uint64_t* const kvempty = kvfull + 8;        // [8] read by S^T and the converters
+    uint64_t* const qkdone = kvempty + 8;        // [4] S^T complete
+    uint64_t* const sempty = qkdone + 4;         // [4] S^T read by the softmax warps
+    uint64_t* const vready = sempty + 4;         // [4] V tile in tensor memory
+    uint64_t* const pready = vready + 4;         // [4] P in shared memory, O rescaled if need be
+    uint64_t* const pvdone = pready + 4;         // [4] O^T has the tile (and the V tile and P are free)
+    uint64_t* const qready = pvdone + 4;         // [2] Q of a segment in shared memory
     uint64_t* const qfree = qready + 2;          // [2] its last S^T is complete
     uint64_t* const ofull = qfree + 2;           // [1] a segment's O^T is complete
     uint64_t* const oempty = ofull + 1;          // [1] read by the softmax warps
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(oempty + 1);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    float2* const tok = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + 512);   // [TOK_RING][128] (K, V scale)
-    float2* const page_scale = tok + C::TOK_RING * KV_TILE;                                  // [8 stages][8 pages]
-    float* const rowf = reinterpret_cast<float*>(page_scale + 64);                           // [ROWF_RING][NT]: score = S * rowf * K scale
-    float* const negm = rowf + C::ROWF_RING * NT;                                                       // [NT] -m
+    float2* const page_scale = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + 512);   // [SCALE_RING][8] (K, V)
+    float* const rowf = reinterpret_cast<float*>(page_scale + C::SCALE_RING * 8);            // [ROWF_RING][NT]: score = S * rowf * K scale
+    float* const negm = rowf + C::ROWF_RING * NT;                                            // [NT] -m
     float* const resc = negm + NT;                                                           // [NT]
     float* const lsum = resc + NT;                                                           // [NT]
     float* const red = lsum + NT;                                                            // [2][4][NH]
@@ -422,9 +450,9 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     // the merge may be brought up now; it waits for this launch's parts by itself
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::STAGES; ++i) { mbar_init(&kvfull[i], 33); mbar_init(&kvempty[i], 8); }
+        for (int i = 0; i < C::STAGES; ++i) { mbar_init(&kvfull[i], 33); mbar_init(&kvempty[i], 5); }
         for (int i = 0; i < BUFS; ++i) {
-            mbar_init(&kready[i], 4); mbar_init(&qkdone[i], 1); mbar_init(&sempty[i], 8);
+            mbar_init(&qkdone[i], 1); mbar_init(&sempty[i], 8);
             mbar_init(&vready[i], 4); mbar_init(&pready[i], 8); mbar_init(&pvdone[i], 1);
         }
         for (int i = 0; i < 2; ++i) { mbar_init(&qready[i], 2); mbar_init(&qfree[i], 1); }
@@ -479,10 +507,10 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             // ------------------------------------------------------------ producer
             const uint64_t pol = p.row_tiles > 1 ? policy_evict_normal() : policy_evict_first();
             const int per_tile = KV_TILE >> p.page_log2;
-            const uint32_t page_bytes = 2u * D << p.page_log2;
+            const uint32_t side_bytes = (uint32_t)D << p.page_log2, piece = 16u << p.page_log2;
             const uint32_t stage0 = smem_u32(stages);
             int s = 0;
-            uint32_t ph = 0, issued = 0, last_ph = 0;
+            uint32_t ph = 0, issued = 0, last_ph = 0, tile = 0;
             bool more = walk.next(sg);
             int k = more ? sg.k0 : 0;
             // the page that this lane brings in of tile k: looked up a tile ahead
@@ -508,15 +536,24 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                     if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_PRODUCER);
                     break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&kvfull[s], page_bytes * (uint32_t)cur_n);
+                if (lane == 0) mbar_arrive_expect_tx(&kvfull[s], 2u * side_bytes * (uint32_t)cur_n);
                 __syncwarp();
+                const uint32_t dst = stage0 + (uint32_t)(s * C::STAGE_BYTES);
+                const size_t unit = (size_t)page * p.heads + head;
+                for (int i0 = 0; i0 < cur_n * (D / 16); i0 += 32) {
+                    const int i = i0 + lane, j = i / (D / 16), c = i % (D / 16);
+                    const uint32_t u_lo = __shfl_sync(0xFFFFFFFFu, (uint32_t)unit, j & 31), u_hi = __shfl_sync(0xFFFFFFFFu, (uint32_t)(unit >> 32), j & 31);
+                    if (j < cur_n)
+                        bulk_load_s(dst + (uint32_t)c * (KV_TILE * 16) + (uint32_t)j * piece,
+                                    p.pages + (((size_t)u_hi << 32) | u_lo) * (2u * side_bytes) + (uint32_t)c * piece, piece, &kvfull[s], pol);
+                }
                 if (lane < cur_n) {
-                    const size_t unit = (size_t)page * p.heads + head;
-                    bulk_load_s(stage0 + (uint32_t)(s * C::STAGE_BYTES) + page_bytes * (uint32_t)lane, p.pages + unit * page_bytes,
-                                page_bytes, &kvfull[s], pol);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(page_scale + 8 * s + lane)),
+                    bulk_load_s(dst + C::SIDE_BYTES + (uint32_t)lane * side_bytes, p.pages + unit * (2u * side_bytes) + side_bytes, side_bytes,
+                                &kvfull[s], pol);
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(page_scale + 8 * (tile % C::SCALE_RING) + lane)),
                                  "l"(p.scales + 2 * unit) : "memory");
                 }
+                ++tile;
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&kvfull[s])) : "memory");
                 issued |= 1u << s;
                 last_ph = (last_ph & ~(1u << s)) | (ph << s);
@@ -530,6 +567,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
         } else if (warp < 3) {
             // ------------------------------------------------------------ MMA issuers
             const uint32_t tmem_u = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            const uint64_t kdesc = kv_uniform64(smem_desc_k_plain(smem_u32(stages), 128u, KV_TILE * 16u));
             const uint64_t qdesc = kv_uniform64(smem_desc_k_sw128(smem_u32(q_sm)));
             const uint64_t pdesc = kv_uniform64(smem_desc_mn_sw32(smem_u32(p_sm), C::P_ATOM, C::P_STEP));
             const bool leader = elect_one();
@@ -541,6 +579,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 }
             };
             KvRing<BUFS> ring;
+            KvRing<C::STAGES> stage;
             uint32_t seg = 0;
             uint64_t* last_bar = nullptr;
             uint32_t last_par = 0;
@@ -549,16 +588,19 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                     const uint32_t b = ring.i;
                     if (warp == 1) {
                         if (k == sg.k0) wait(&qready[seg & 1u], (seg >> 1) & 1u);
-                        wait(&kready[b], ring.par);
+                        wait(&kvfull[stage.i], stage.par);
                         wait(&sempty[b], ring.par ^ 1u);
                         if (!ok) break;
                         tc_fence_after();
                         if (leader) {
+                            const uint64_t kd = kdesc + (uint64_t)(stage.i * (C::STAGE_BYTES >> 4));
                             const uint64_t qd = qdesc + (uint64_t)((seg & 1u) * (C::Q_BYTES >> 4));
+                            const uint32_t d = tmem_u + (uint32_t)(C::S_COL) + b * NT;
 #pragma unroll
-                            for (int i = 0; i < D / 16; ++i)
-                                mma_ts_f16(tmem_u + (uint32_t)(C::S_COL) + b * NT, tmem_u + (uint32_t)(C::K_COL + 8 * i) + b * C::K_COLS,
-                                           qd + (uint64_t)(((i >> 2) * NT * 128 + (i & 3) * 32) >> 4), C::IDESC, i ? 1u : 0u);
+                            for (int i = 0; i < C::QSTEPS; ++i)
+                                mma_ss_f8(d, kd + (uint64_t)(((i % (D / 32)) * 2 * KV_TILE * 16) >> 4),
+                                          qd + (uint64_t)(((i >> 2) * NT * 128 + (i & 3) * 32) >> 4), C::IDESC_QK, i ? 1u : 0u);
+                            mma_commit(&kvempty[stage.i]);
                             mma_commit(&qkdone[b]);
                             if (k + 1 == sg.k1) mma_commit(&qfree[seg & 1u]);
                         }
@@ -574,7 +616,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
 #pragma unroll
                             for (int i = 0; i < KV_TILE / 16; ++i)
                                 mma_ts_f16(tmem_u + (uint32_t)C::O_COL, tmem_u + (uint32_t)(C::V_COL + 8 * i) + b * C::V_COLS,
-                                           pd + (uint64_t)((2 * i * C::P_STEP) >> 4), C::IDESC_P, (i || k != sg.k0) ? 1u : 0u);
+                                           pd + (uint64_t)((2 * i * C::P_STEP) >> 4), C::IDESC_PV, (i || k != sg.k0) ? 1u : 0u);
                             mma_commit(&pvdone[b]);
                             if (k + 1 == sg.k1) mma_commit(ofull);
                         }
@@ -583,6 +625,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                     last_par = ring.par;
                     __syncwarp();
                     ring.step();
+                    stage.step();
                 }
                 ++seg;
             }
@@ -609,14 +652,12 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     } else if (warp < 12) {
         // ------------------------------------------------------------ converters
         regs_dec<C::REGS_CONVERT>();
-        const bool is_v = warp >= 8;
-        const int qd = warp & 3, r = 32 * qd + lane;             // K: token of the tile; V: channel
+        const uint32_t set = (uint32_t)(warp - 4) >> 2;
+        const int qd = warp & 3, r = 32 * qd + lane;             // channel
         const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16);
-        const int pl = p.page_log2;
-        const uint32_t page_bytes = 2u * D << pl;
-        int s = 0;
-        uint32_t ph = 0, n = 0;
+        KvRing<C::STAGES> stage;
         KvRing<BUFS> ring;
+        uint32_t n = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             if (!__all_sync(0xFFFFFFFFu, kv_wait(bar, parity, abort_flag))) {
@@ -625,52 +666,25 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             }
         };
         while (ok && walk.next(sg)) {
-            for (int k = sg.k0; k < sg.k1; ++k) {
+            for (int k = sg.k0; k < sg.k1; ++k, ++n, stage.step(), ring.step()) {
+                if ((n & 1u) != set) continue;
                 const uint32_t b = ring.i;
-                wait(&kvfull[s], ph);
+                wait(&kvfull[stage.i], stage.par);
                 if (!ok) break;
-                const uint8_t* const st = stages + s * C::STAGE_BYTES;
+                uint4 w[8];
+                if (D == 128 || qd < 2) {
+                    const uint8_t* const at = stages + stage.i * C::STAGE_BYTES + C::SIDE_BYTES + 16 * r;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4*>(at + 16 * D * c);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kvempty[stage.i]);
+                // tokens behind the request's last one count nothing, whatever their bytes are
+                const int valid = (k + 1 == sg.tiles) ? last8[sg.b] : KV_TILE;
                 uint32_t out[32];
-                if (!is_v) {
-                    const uint8_t* const at = st + (uint32_t)(r >> pl) * page_bytes + (uint32_t)(r & ((1 << pl) - 1)) * 16u;
-                    uint4 w[8];
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) w[c] = *reinterpret_cast<const uint4*>(at + ((16u * c) << pl));
-                    const float2 sc = page_scale[8 * s + (r >> pl)];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&kvempty[s]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) kv_decode16(w[c], out + 8 * c);
-                    wait(&qkdone[b], ring.par ^ 1u);              // the S^T that read this K buffer last
-                    if (!ok) break;
-                    tc_fence_after();
-                    // that S^T, of tile n - BUFS, had its buffer from tile n - 2 BUFS, whose scales are thus read: at most
-                    // 2 BUFS tiles' scales are in use
-                    tok[(n % C::TOK_RING) * KV_TILE + r] = sc;
-                    tmem_st32(t_lane + (uint32_t)C::K_COL + b * C::K_COLS, out);
-                    if (D == 128) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) kv_decode16(w[4 + c], out + 8 * c);
-                        tmem_st32(t_lane + (uint32_t)C::K_COL + b * C::K_COLS + 32u, out);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&kready[b]);
-                } else if (D == 128 || qd < 2) {
-                    // tokens behind the request's last one count nothing, whatever their bytes are
-                    const int valid = (k + 1 == sg.tiles) ? last8[sg.b] : KV_TILE;
-                    uint4 w[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int t = 16 * c;
-                        w[c] = *reinterpret_cast<const uint4*>(st + (uint32_t)(t >> pl) * page_bytes + (uint32_t)(D << pl) +
-                                                               (uint32_t)((t & ((1 << pl) - 1)) >> 4) * (16u * D) + 16u * r);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&kvempty[s]);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                for (int half = 0; half < 2; ++half) {
+                    if (D == 128 || qd < 2) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) kv_decode16(w[4 * half + c], out + 8 * c);
                         if (valid < KV_TILE) {
@@ -681,30 +695,21 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                                 else if (t + 1 >= valid) out[j] &= 0xFFFFu;
                             }
                         }
-                        if (half == 0) {
-                            wait(&pvdone[b], ring.par ^ 1u);      // the O^T that read this V buffer last
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-                        tmem_st32(t_lane + (uint32_t)C::V_COL + b * C::V_COLS + 32u * half, out);
                     }
-                    if (!ok) break;
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&vready[b]);
-                } else {
-                    // no channels of this quarter: the stage and the buffer pass as they are, in step with the others (an
-                    // arrival ahead of its phase would complete another tile's)
-                    if (lane == 0) mbar_arrive(&kvempty[s]);
-                    wait(&pvdone[b], ring.par ^ 1u);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive(&vready[b]);
+                    if (half == 0) {
+                        // the O^T that read this V buffer last; a quarter without channels waits too, for an arrival ahead
+                        // of its phase would complete another tile's
+                        wait(&pvdone[b], ring.par ^ 1u);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    if (D == 128 || qd < 2) tmem_st32(t_lane + (uint32_t)C::V_COL + b * C::V_COLS + 32u * half, out);
                 }
+                if (!ok) break;
+                tmem_wait_st();
+                tc_fence_before();
                 __syncwarp();
-                ++n;
-                ring.step();
-                if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+                if (lane == 0) mbar_arrive(&vready[b]);
             }
         }
         tmem_wait_st();
@@ -743,7 +748,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 float x[NH];
 #pragma unroll
                 for (int i = 0; i < NH; i += 8) tmem_ld8(t_lane + (uint32_t)(C::S_COL + c0 + i) + b * NT, x + i);
-                const float2 sc = tok[(n % C::TOK_RING) * KV_TILE + t];
+                const float2 sc = page_scale[8 * (n % C::SCALE_RING) + (t >> p.page_log2)];
                 const int valid = (k + 1 == sg.tiles) ? last8[sg.b] : KV_TILE;
                 const bool live = t < valid;
                 const float vs = live ? sc.y : 1.0f;
@@ -896,24 +901,34 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     }
 }
 
-// One warp per (row, query head): the scores of the tree nodes that the row sees (a lane a node), their
-// softmax and V in fp32, then the parts of the cached tokens, in list order. A node that the mask leaves
-// out is never read, so nothing of it (an infinity, a NaN) reaches the row. A row that sees nothing at
-// all gives zeros.
-constexpr int KV_MERGE_THREADS = 256;
+// One warp per row of a unit, a CTA's rows all of one unit, so that they share the tree's K and V of the KV head in
+// shared memory: the scores of the nodes that the row sees (a lane a node), their softmax and V in fp32, then the
+// parts of the cached tokens, in list order. What the mask leaves out is never used, so nothing of it (an infinity, a
+// NaN) reaches the row. A row that sees nothing at all gives zeros. Latency-bound: all of it up to the parts runs
+// while the streaming kernel does.
+constexpr int KV_MERGE_WARPS = 8, KV_MERGE_THREADS = 32 * KV_MERGE_WARPS;
 
 template <int D>
-__global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttnParams p) {
+__global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttnParams p, int chunks) {
     constexpr int E = D / 32;                            // channels of a lane
-    __shared__ long long sums[2][KV_MERGE_THREADS / 32];
+    constexpr int RP = D + 8;                            // padded row: 16-byte reads of eight rows spread over the banks
+    __shared__ __align__(16) __nv_bfloat16 kn[KV_MAX_ROWS * RP], vn[KV_MAX_ROWS * RP];
+    __shared__ long long sums[2][KV_MERGE_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x;
+    const int b = blockIdx.x, head = blockIdx.y / chunks, chunk = blockIdx.y % chunks;
     int first;
     bool bad = false;
     const int rows = kv_rows_of(p, b, &first, &bad);
     if (bad && tid == 0 && blockIdx.y == 0) atomicCAS(p.err, 0, TL_DEV_ERR_KV_ROWS);
-    const int per = blockIdx.y * (KV_MERGE_THREADS / 32) + warp;    // (row, query head) of the request
-    if (blockIdx.y * (KV_MERGE_THREADS / 32) >= rows * p.heads * p.group) return;
+    if (chunk * KV_MERGE_WARPS >= rows * p.group) return;
+    if (p.k_new) {
+        for (int e = tid; e < rows * (D / 8); e += KV_MERGE_THREADS) {
+            const int j = e / (D / 8), c = e % (D / 8);
+            const size_t at = (size_t)(first + j) * p.new_stride + (size_t)head * D + 8 * c;
+            *reinterpret_cast<uint4*>(kn + j * RP + 8 * c) = __ldg(reinterpret_cast<const uint4*>(p.k_new + at));
+            *reinterpret_cast<uint4*>(vn + j * RP + 8 * c) = __ldg(reinterpret_cast<const uint4*>(p.v_new + at));
+        }
+    }
     // this request's place in the tile list
     long long before = 0, all = 0;
     for (int i = tid; i < p.B; i += KV_MERGE_THREADS) {
@@ -930,39 +945,36 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
     __syncthreads();
     all = before = 0;
 #pragma unroll
-    for (int u = 0; u < KV_MERGE_THREADS / 32; ++u) { all += sums[0][u]; before += sums[1][u]; }
-    const int hq = p.heads * p.group;
-    const bool mine = per < rows * hq;
-    const int i = mine ? per / hq : 0, h = mine ? per % hq : 0, head = h / p.group;
+    for (int u = 0; u < KV_MERGE_WARPS; ++u) { all += sums[0][u]; before += sums[1][u]; }
+    const int r = chunk * KV_MERGE_WARPS + warp;
+    if (r >= rows * p.group) return;
+    const int i = r / p.group, h = head * p.group + r % p.group;
     const int row = first + i;
 
     float m = -INFINITY, l = 0.0f;
     float o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    if (mine && p.k_new) {
+    if (p.k_new) {
         unsigned bits = p.mask ? p.mask[row] : (2u << i) - 1u;
         if (rows < 32) bits &= (1u << rows) - 1u;
-        float s = -INFINITY;
-        if ((bits >> lane) & 1u) {
-            const uint4* const kr = reinterpret_cast<const uint4*>(p.k_new + (size_t)(first + lane) * p.new_stride + (size_t)head * D);
-            const uint4* const qr = reinterpret_cast<const uint4*>(p.q + (size_t)row * p.q_stride + (size_t)h * D);
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const bool sees = (bits >> lane) & 1u;
+        const uint4* const qr = reinterpret_cast<const uint4*>(p.q + (size_t)row * p.q_stride + (size_t)h * D);
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (sees) {
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
-                const uint4 a = __ldg(kr + c), w = __ldg(qr + c);
+                const uint4 a = *reinterpret_cast<const uint4*>(kn + lane * RP + 8 * c), w = __ldg(qr + c);
                 const uint32_t ka[4] = {a.x, a.y, a.z, a.w}, qa[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
                     acc[u] = fmaf(__int_as_float((int)(ka[u] & 0xFFFF0000u)), __int_as_float((int)(qa[u] & 0xFFFF0000u)),
                                   fmaf(__int_as_float((int)(ka[u] << 16)), __int_as_float((int)(qa[u] << 16)), acc[u]));
             }
-            s = ((acc[0] + acc[1]) + (acc[2] + acc[3])) * p.scale;
         }
-        float top = s;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        const float pr = ((bits >> lane) & 1u) ? exp2f(s - top) : 0.0f;
+        const float s = sees ? ((acc[0] + acc[1]) + (acc[2] + acc[3])) * p.scale : -INFINITY;
+        const float top = kv_warp_max(s);
+        const float pr = sees ? exp2f(s - top) : 0.0f;
         float sum = pr;
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
@@ -970,10 +982,9 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
         for (unsigned todo = bits; todo; todo &= todo - 1) {
             const int j = __ffs(todo) - 1;
             const float w = __shfl_sync(0xFFFFFFFFu, pr, j);
-            const __nv_bfloat16* const vr = p.v_new + (size_t)(first + j) * p.new_stride + (size_t)head * D + E * lane;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
-                const uint32_t x = __ldg(reinterpret_cast<const unsigned*>(vr + e));
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(vn + j * RP + E * lane + e);
                 o[e] = fmaf(w, __int_as_float((int)(x << 16)), o[e]);
                 o[e + 1] = fmaf(w, __int_as_float((int)(x & 0xFFFF0000u)), o[e + 1]);
             }
@@ -982,13 +993,12 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
     // the parts of the cached tokens
     const int len = kv_len_of(p, b);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!mine) return;
     if (len > 0) {
         const int tiles = kv_tiles(len);
         const long long total = (long long)p.heads * all, groups = p.groups < total ? p.groups : total;
         const long long a = (long long)p.heads * before + (long long)head * tiles, z = a + tiles;
         const int g0 = (int)(((a + 1) * groups - 1) / total), g1 = (int)((z * groups - 1) / total);
-        const int r = i * p.group + h % p.group, rt = r / p.nt, n = r % p.nt;
+        const int rt = r / p.nt, n = r % p.nt;
         // four parts' loads in flight at once
         for (int g = g0; g <= g1; g += 4) {
             float2 ml[4], x[4][E / 2];

@@ -1313,8 +1313,8 @@ tl_status launch_kv_attention(const tl::KvAttnParams& p, cudaStream_t stream) {
                  : p.nt == 64 ? launch_kv_stream<D, 64>(p, stream)
                               : launch_kv_stream<D, 80>(p, stream);
     if (st != TL_OK) return st;
-    const int warps = tl::KV_MERGE_THREADS / 32;
-    const dim3 grid((unsigned)p.B, (unsigned)((p.max_rows * p.heads * p.group + warps - 1) / warps));
+    const int chunks = (p.max_rows * p.group + tl::KV_MERGE_WARPS - 1) / tl::KV_MERGE_WARPS;
+    const dim3 grid((unsigned)p.B, (unsigned)(p.heads * chunks));
     // brought up while the streaming kernel runs: it works on the tree's own rows, then waits for the parts
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1326,7 +1326,7 @@ tl_status launch_kv_attention(const tl::KvAttnParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    TL_CUDA(cudaLaunchKernelEx(&cfg, tl::kv_merge_kernel<D>, p));
+    TL_CUDA(cudaLaunchKernelEx(&cfg, tl::kv_merge_kernel<D>, p, chunks));
     return TL_OK;
 }
 

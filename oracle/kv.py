@@ -132,12 +132,13 @@ def cached(pages, scales, P, D, ids, n, head, side):
 
 
 def attention(q, pages, scales, P, table, lens, k_new, v_new, masks, row_start, scale):
-    """(out, weight, size): out float64 [R, heads, D]; weight = sum p |v| / sum p, and size [R, heads] = the largest
-    scale * sum |q k| over what the row sees: what the error of a computed result is measured by."""
+    """(out, weight, size, reach): out float64 [R, heads, D]; weight = sum p |v| / sum p; of what the row sees, size
+    [R, heads] = the largest scale * sum |q k| and reach = the largest scale * max |q| * sum |k|: what the error of a
+    computed result is measured by."""
     R, Hq, D = q.shape
     heads = pages.shape[1]
     g = Hq // heads
-    out, weight, size = np.zeros((R, Hq, D)), np.zeros((R, Hq, D)), np.zeros((R, Hq))
+    out, weight, size, reach = np.zeros((R, Hq, D)), np.zeros((R, Hq, D)), np.zeros((R, Hq)), np.zeros((R, Hq))
     for b, n in enumerate(lens):
         lo, hi = int(row_start[b]), int(row_start[b + 1])
         for h in range(heads):
@@ -156,4 +157,5 @@ def attention(q, pages, scales, P, table, lens, k_new, v_new, masks, row_start, 
                     out[i, a] = p @ v / p.sum()
                     weight[i, a] = p @ np.abs(v) / p.sum()
                     size[i, a] = abs(scale) * np.max(np.abs(k) @ np.abs(x))
-    return out, weight, size
+                    reach[i, a] = abs(scale) * np.max(np.abs(x)) * np.max(np.abs(k).sum(1))
+    return out, weight, size, reach

@@ -2,14 +2,18 @@
 64-bit statements in oracle/kv.py.
 
 Bars. Slot maps and commits are exact: every page id, slot, byte and scale is compared. Attention, per element, with W = sum
-p |v| / sum p and A = the largest scale * sum |q k| of the row, both from the oracle, over n cached tokens of D channels:
+p |v| / sum p, A = the largest scale * sum |q k| of the row and C = the largest scale * max |q| * sum |k|, from the oracle,
+over n cached tokens of D channels:
 
-    |y - y_ref| <= 2^-8 |y_ref| + W (2^-11 + 4 * 2^-24 * (D A + n) + 2^-19)
+    |y - y_ref| <= 2^-8 |y_ref| + W (2^-11 + 4 * 2^-24 * (D A + n) + 2^-19 + 2^-16.8 C)
 
 The terms: bf16 output, half a step 2^-8. Weights p rounded to f16 for the product with V, half a step 2^-11. A score is D
 products (exact in fp32) summed in fp32, each addition within 2^-23 (a truncating adder), so it is off by D 2^-23 A and its p by
 as much, once above and once below the division: 4 * 2^-24 D A. Sums over n tokens above and below: the same with n. exp2, its
-argument's rounding, the division and the factors: within 2^-19 for arguments up to 2^4, times W.
+argument's rounding, the division and the factors: within 2^-19 for arguments up to 2^4, times W. Q is held in two E4M3
+terms under a scale that brings the row's largest magnitude above 224: the second term's smallest step is 2^-9, so an element
+is off by at most 2^-10 / 224 < 2^-17.8 of the largest, a score by 2^-17.8 C, and y by twice that (above and below the
+division).
 """
 
 import math
@@ -294,11 +298,12 @@ class Case:
                             self.start, self.scale)
 
     def check(self, y, ref=None):
-        out, weight, size = self.reference() if ref is None else ref
+        out, weight, size, reach = self.reference() if ref is None else ref
         n = np.zeros(len(out))
         for b, m in enumerate(self.lens):
             n[self.start[b] : self.start[b + 1]] = m + 32
-        bar = 2.0 ** -8 * np.abs(out) + weight * (2.0 ** -11 + 4 * 2.0 ** -24 * (self.D * size + n[:, None]) + 2.0 ** -19)[..., None]
+        off = 2.0 ** -11 + 4 * 2.0 ** -24 * (self.D * size + n[:, None]) + 2.0 ** -19 + 2.0 ** -16.8 * reach
+        bar = 2.0 ** -8 * np.abs(out) + weight * off[..., None]
         got = y.float().cpu().numpy().astype(np.float64)
         bad = ~(np.abs(got - out) <= bar)
         assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], out[bad][:4], bar[bad][:4])
@@ -377,17 +382,17 @@ def test_attention_rows_that_see_nothing_and_nan_in_unseen_nodes():
         y = c.run()
         masks_seen = [0x1, 0x2, 0x0, 0x9]
         c.masks = np.array(masks_seen)
-        out, weight, size = c.reference()
+        out, weight, size, reach = c.reference()
         got = y.float().cpu().numpy()
         assert np.isnan(got[1]).all()
         keep = [0, 2, 3]
         assert np.isfinite(got[keep]).all()
         if n == 0:
             assert not got[2].any()
-        out[1] = weight[1] = size[1] = 0.0
+        out[1] = weight[1] = size[1] = reach[1] = 0.0
         z = y.clone()
         z[1] = 0
-        c.check(z, (out, weight, size))
+        c.check(z, (out, weight, size, reach))
 
 
 def test_attention_nan_in_a_seen_token_reaches_every_row_of_its_head_only():

@@ -211,8 +211,8 @@ def test_attention_hand_worked():
     pages[0, 0, 1, kv.place_v(0, np.array([3]), D)] = one    # token 0: v = e_3
     q = np.zeros((2, 1, D)); q[0, 0, 0] = math.log(3.0)
     kn = np.zeros((2, 1, D)); vn = np.zeros((2, 1, D)); vn[0, 0, 5] = 2.0; vn[1] = np.nan
-    out, _, _ = kv.attention(q, pages, scales, P, np.array([[0]]), [1], kn, vn, [1, 0], [0, 2], 1.0)
+    out, _, _, _ = kv.attention(q, pages, scales, P, np.array([[0]]), [1], kn, vn, [1, 0], [0, 2], 1.0)
     # row 0: token 0 with weight 3, itself with weight 1; row 1 sees token 0 alone
     assert np.allclose(out[0, 0, [3, 5]], [0.75, 0.5]) and np.allclose(out[1, 0, 3], 1.0) and np.isfinite(out).all()
-    out, _, _ = kv.attention(q, pages, scales, P, np.array([[0]]), [0], kn, vn, [1, 0], [0, 2], 1.0)
+    out, _, _, _ = kv.attention(q, pages, scales, P, np.array([[0]]), [0], kn, vn, [1, 0], [0, 2], 1.0)
     assert out[0, 0, 5] == 2.0 and not out[1].any()          # nothing to see: zeros
