@@ -19,12 +19,12 @@
 // Two launches: kv_attention_kernel streams the cache and writes one (m, l, O) per part and row;
 // kv_merge_kernel adds the tree and joins the parts.
 //
-// Work. A unit is (request, KV head); its cached tokens are cut into tiles of 128. The tiles of all
-// units form one list, cut into equal contiguous ranges, one for each group of CTAs, so requests of
-// unequal lengths fill the GPU evenly. The group's CTAs take a row tile of the unit's rows each (the
-// rows of a unit are the request's rows times the query heads of its KV head, row r = i * G + g). The
-// part of unit u in range g goes to slot u + g: going along the list, each step moves to the next unit
-// or the next range, so no two parts meet.
+// Work. A unit is (request, KV head, row tile): the rows of a request and KV head are its rows times the head's
+// query heads, row r = i * G + g, in the fewest row tiles that hold them, evenly; the cached tokens are cut into
+// tiles of 128. The tiles of all units form one list, in which a tile weighs what its rows make it cost and a unit some
+// more for its beginning and end; each CTA takes an equal, contiguous share of the weight (the tiles that begin in it),
+// so requests of unequal lengths and trees fill the GPU evenly. The part of unit u on CTA g goes to slot u + g: going
+// along the list, each step moves to the next unit or the next CTA, so no two parts meet.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -50,79 +50,135 @@ struct KvAttnParams {
     const unsigned* mask;         // [R], or null: row i sees rows 0..i
     const int* row_start;         // [B + 1], or null: max_rows rows each
     __nv_bfloat16* out;           // [R][Hq][D], rows out_stride apart
-    float* part_o;                // [slots][row tiles][NT][D]
-    float2* part_ml;              // [slots][row tiles][NT]
+    float* part_o;                // [slots][NT][D]
+    float2* part_ml;              // [slots][NT]
     int* err;
     long long q_stride, new_stride, out_stride;
     float scale;                  // c * log2(e)
-    int B, width, n_pages, page_log2, heads, group, R, max_rows, groups, row_tiles, nt;
+    int B, width, n_pages, page_log2, heads, group, R, max_rows, ctas, row_tiles, nt;   // row tiles of the largest request
 };
 
-// The rows of request b: first row and count (0 where the offsets are invalid).
-__device__ __forceinline__ int kv_rows_of(const KvAttnParams& p, int b, int* first, bool* bad) {
-    if (!p.row_start) {
-        *first = b * p.max_rows;
-        return p.max_rows;
-    }
-    const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
-    *first = r0;
-    if (r0 < 0 || r1 < r0 || r1 - r0 > p.max_rows || r1 > p.R) {
-        *bad = true;
-        return 0;
-    }
-    return r1 - r0;
-}
-
-// The cached tokens of request b that its rows attend to (0 if it has no rows).
-__device__ __forceinline__ int kv_len_of(const KvAttnParams& p, int b) {
-    int first;
-    bool bad = false;
-    if (kv_rows_of(p, b, &first, &bad) == 0) return 0;
-    const long long room = (long long)p.width << p.page_log2;
-    const int len = p.lens[b];
-    return len < 0 ? 0 : (int)(len < room ? len : room);
-}
-
-__device__ __forceinline__ int kv_tiles(int len) { return (int)(((long long)len + KV_TILE - 1) / KV_TILE); }
-
-__device__ __forceinline__ long long kv_range_start(long long g, long long total, long long groups) {
-    return g * total / groups;
-}
-
-// One step of a walk along a range of the tile list: tiles k0..k1 of unit (b, head).
-struct KvSeg {
-    int b, head, k0, k1, tiles;
-};
-
-struct KvSegIter {
-    const int* pre;      // [B + 1] tiles of the requests in front (per head)
-    int heads, b, head, k, left;   // left: tiles to go (a range's share is far below 2^31)
-    __device__ __forceinline__ KvSegIter(const int* pre_, int B, int heads_, long long begin, long long end)
-        : pre(pre_), heads(heads_), b(0), head(0), k(0), left((int)(end - begin)) {
-        if (left <= 0) return;
-        b = kv_find(pre, B, (int)(begin / heads));
-        const int tiles = pre[b + 1] - pre[b];
-        const long long in = begin - (long long)heads * pre[b];
-        head = (int)(in / tiles);
-        k = (int)(in - (long long)head * tiles);
-    }
-    __device__ __forceinline__ bool next(KvSeg& s) {
-        if (left <= 0) return false;
-        int tiles;
-        while ((tiles = pre[b + 1] - pre[b]) == 0) ++b;
-        s.b = b;
-        s.head = head;
-        s.tiles = tiles;
-        s.k0 = k;
-        s.k1 = min(tiles, k + left);
-        left -= s.k1 - k;
-        k = s.k1;
-        if (k == tiles) {
-            k = 0;
-            if (++head == heads) { head = 0; ++b; }
+// Request b: its rows (0 where the offsets are invalid) and the cached tokens they attend to (0 without rows). Its loads
+// do not wait for one another.
+struct KvRequest {
+    int first, rows, len;
+    bool bad;
+    __device__ __forceinline__ KvRequest(const KvAttnParams& p, int b) {
+        const int held = p.lens[b];
+        first = b * p.max_rows;
+        rows = p.max_rows;
+        bad = false;
+        if (p.row_start) {
+            const int r0 = p.row_start[b], r1 = p.row_start[b + 1];
+            bad = r0 < 0 || r1 < r0 || r1 - r0 > p.max_rows || r1 > p.R;
+            first = r0;
+            rows = bad ? 0 : r1 - r0;
         }
+        const long long room = (long long)p.width << p.page_log2;
+        len = (rows == 0 || held < 0) ? 0 : (int)(held < room ? held : room);
+    }
+};
+
+__device__ __forceinline__ int kv_tiles(int len) { return (int)(((unsigned)len + KV_TILE - 1) / KV_TILE); }
+
+// Weights, in about 200 cycles: a tile's share that does not depend on its rows, and a unit's beginning and end.
+constexpr int KV_W_TILE = 4, KV_W_UNIT = 12;
+
+// How the rows of a request are cut for row tiles of at most `most` rows, and what its units weigh. (The host keeps the
+// weight of a whole call below 2^32.)
+struct KvShape {
+    int row_tiles, nt;      // row tiles, and rows of each (a multiple of 16; the last may hold fewer)
+    unsigned tile_w, unit_w;
+    __device__ __forceinline__ KvShape() {}
+    __device__ __forceinline__ KvShape(int rows, int tiles, int most) {
+        row_tiles = (rows + most - 1) / most;
+        nt = row_tiles <= 1 ? (rows + 15) / 16 * 16 : ((rows + row_tiles - 1) / row_tiles + 15) / 16 * 16;
+        tile_w = KV_W_TILE + nt / 16;
+        unit_w = KV_W_UNIT + tiles * tile_w;
+    }
+    // Of a unit that begins at weight 0, the first tile that begins at `x` or behind it.
+    __device__ __forceinline__ int tile_from(unsigned x, int tiles) const {
+        if (x == 0) return 0;
+        if (x >= unit_w) return tiles;
+        return x <= KV_W_UNIT + tile_w ? 1 : (int)((x - KV_W_UNIT + tile_w - 1) / tile_w);
+    }
+};
+
+// The shares of the CTAs: of `total`, CTA g has start(g) .. start(g + 1), equal to within one.
+struct KvShares {
+    unsigned q, r;
+    __device__ __forceinline__ KvShares(unsigned total, int ctas) : q(total / ctas), r(total % ctas) {}
+    __device__ __forceinline__ unsigned start(int g) const { return (unsigned)g * q + min((unsigned)g, r); }
+    __device__ __forceinline__ int owner(unsigned x) const { return x < r * (q + 1) ? (int)(x / (q + 1)) : (int)(r + (x - r * (q + 1)) / q); }
+};
+
+// One step of a walk along a range of the tile list: tiles k0..k1 of row tile rt of (b, head).
+struct KvSeg {
+    int b, head, rt, k0, k1, tiles, nt, n_rows;
+};
+
+struct KvWalk {
+    const unsigned* pre;     // [B + 1] weight of the requests in front
+    const int* len;          // [B]
+    const uint8_t* rows;     // [B]
+    int B, heads, group, most;
+    unsigned end;
+    int b, head, rt, k;      // next: tile k of unit (b, head, rt)
+    int tiles;               // of request b
+    unsigned at;             // where its unit begins
+    KvShape s;
+    __device__ __forceinline__ void look() {
+        tiles = kv_tiles(len[b]);
+        s = KvShape((int)rows[b] * group, tiles, most);
+    }
+    __device__ __forceinline__ KvWalk(const KvAttnParams& p, const unsigned* pre_, const int* len_, const uint8_t* rows_, unsigned begin,
+                                      unsigned end_, int most_)
+        : pre(pre_), len(len_), rows(rows_), B(p.B), heads(p.heads), group(p.group), most(most_), end(end_), b(p.B), head(0), rt(0), k(0),
+          tiles(0), at(0) {
+        if (begin >= end) return;
+        int lo = 0, hi = B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= begin) lo = mid; else hi = mid;
+        }
+        b = lo;
+        look();
+        const unsigned in = begin - pre[b], j = in / s.unit_w;
+        head = (int)(j / s.row_tiles);
+        rt = (int)(j - head * s.row_tiles);
+        at = pre[b] + j * s.unit_w;
+        k = s.tile_from(begin - at, tiles);
+        if (k == tiles) step();
+    }
+    // on to the next unit
+    __device__ __forceinline__ void step() {
+        k = 0;
+        at += s.unit_w;
+        if (++rt < s.row_tiles) return;
+        rt = 0;
+        if (++head < heads) return;
+        head = 0;
+        do ++b; while (b < B && pre[b + 1] == pre[b]);
+        if (b < B) look();
+    }
+    __device__ __forceinline__ bool next(KvSeg& g) {
+        if (b >= B || at >= end) return false;
+        const int k1 = s.tile_from(end - at, tiles);
+        if (k1 <= k) return false;
+        g.b = b;
+        g.head = head;
+        g.rt = rt;
+        g.k0 = k;
+        g.k1 = k1;
+        g.tiles = tiles;
+        g.nt = s.nt;
+        g.n_rows = min((int)rows[b] * group - rt * s.nt, s.nt);
+        k = k1;
+        if (k == tiles) step();
         return true;
     }
+    // tokens of the last tile of request b_
+    __device__ __forceinline__ int last(int b_) const { return ((len[b_] - 1) & (KV_TILE - 1)) + 1; }
 };
 
 // ---------------------------------------------------------------- the streaming kernel
@@ -130,10 +186,11 @@ struct KvSegIter {
 // Both products run on the tensor cores with the cache as operand A and the rows as operand B, so that
 // few rows cost little (an MMA is 128 tokens or channels times NT rows, NT a multiple of 16):
 //
-//     S^T [token][row]   = K  [token][channel] . Q^T      E4M3: A = the cache's bytes in shared memory as they are
+//     S^T [token][row]   = K  [token][channel] . Q^T      E4M3: A = the cache's bytes, moved to tensor memory as they are
 //     O^T [channel][row] = V^T [channel][token] . P^T     f16:  A = V in tensor memory,  B = P in shared memory
 //
-// K is never converted: Q is. Each row of Q is scaled by a power of two that brings its largest magnitude into
+// K is never converted: Q is. (K fed from shared memory would need a tile's pages in pieces of 16 channels, and bulk copies
+// that small, 18 a tile, took the decode case from 140 to 172 us.) Each row of Q is scaled by a power of two that brings its largest magnitude into
 // (224, 448] and written as the sum of two E4M3 terms, the second holding what the first left over. A bf16 value
 // has 8 significant bits and a term holds 4, so the sum is exact for elements down to 2^-10 of the largest; the
 // others are within 2^-10 in that scale, 2^-17.8 of the row's largest. Both terms multiply the same K into one fp32
@@ -146,16 +203,17 @@ struct KvSegIter {
 // KV_SLACK; only then (and in a segment's first tile) are the tile's maxima found across lanes, and O and
 // l rescaled. So most tiles need one comparison a score and one vote.
 //
-// Roles (one CTA of 20 warps per SM; registers are moved between the warpgroups, KvCfg):
-//   * warp 0        producer: bulk copies of a tile's pages (128 tokens) into a ring of stages: K in pieces of 16
-//                   channels, so that a tile of several pages is one operand, V a piece a page. Scales follow by cp.async.
+// Roles (one CTA of 16 warps per SM; registers are moved between the warpgroups, KvCfg):
+//   * warp 0        producer: a page's K and V of the head are one contiguous piece, brought in by one bulk copy;
+//                   tiles of 128 tokens, a ring of stages. Scales follow by cp.async.
 //   * warp 1        issues the MMAs of S^T, warp 2 those of O^T (an issuer manages one MMA in some 55 cycles while
 //                   other warps run, so one warp for all sixteen of a tile was a bound).
 //   * warp 3        the rows: Q of the next segment to one of two buffers in shared memory. The first segment's Q is
 //                   brought in by the softmax warps, which have nothing to do yet.
-//   * warps 4..11   V converters, two sets of four that take turns; lane = channel, 16 bytes of a lane at a time.
-//   * warps 12..19  softmax: two groups of four warps, half of the rows each, lane = token. A group also reads its
-//                   rows of O (lane = channel) when a segment ends and writes the part.
+//   * warps 4..7    movers: K (lane = token), then V, converted (lane = channel), 16 bytes of a lane at a time.
+//   * warps 8..15   softmax: two groups of four warps, every other block of 8 rows each, lane = token; blocks without rows
+//                   are passed over. A group also reads its rows of O (lane = channel) when a segment ends and writes
+//                   the part.
 // Every mbarrier wait is bounded; after one has run out the others return at once, every role runs to its end
 // (so no named barrier is left waiting), and the status word is set.
 
@@ -164,24 +222,24 @@ constexpr float KV_P_SHIFT = 8.0f;
 
 template <int D, int NT>
 struct KvCfg {
-    static constexpr int WARPS = 20, THREADS = 32 * WARPS;
-    // registers a thread: 96 at launch (480 over the five warpgroups), then dealt out by need
-    static constexpr int REGS_CONTROL = 64, REGS_CONVERT = 80, REGS_SOFTMAX = 128;
-    static_assert(REGS_CONTROL + 2 * REGS_CONVERT + 2 * REGS_SOFTMAX <= 480, "registers of the launch");
+    static constexpr int WARPS = 16, THREADS = 32 * WARPS;
+    // registers a thread: 128 at launch (512 over the four warpgroups), then dealt out by need
+    static constexpr int REGS_CONTROL = 96, REGS_MOVE = 96, REGS_SOFTMAX = 160;
+    static_assert(REGS_CONTROL + REGS_MOVE + 2 * REGS_SOFTMAX <= 512, "registers of the launch");
     static constexpr int NH = NT / 2;                          // rows of a softmax group
-    static constexpr int SIDE_BYTES = KV_TILE * D;             // K of a tile: [D/16][128][16]; V: [8][D][16]
-    static constexpr int STAGE_BYTES = 2 * SIDE_BYTES;
+    static constexpr int NB = NT / 16;                         // blocks of 8 of a softmax group
+    static constexpr int STAGE_BYTES = 2 * KV_TILE * D;
     static constexpr int QSTEPS = 2 * D / 32;                  // MMAs of S^T: 32 channels each, both terms
     static constexpr int Q_BYTES = NT * D * 2;                 // slabs of [NT] 128-byte rows, swizzled: the first terms, the second
     static constexpr int P_BYTES = NT * KV_TILE * 2;
     // tiles in flight between converters, MMAs and softmax: what tensor memory (and for 80 rows shared memory) holds
-    static constexpr int BUFS = (4 * (KV_TILE / 2 + NT) + NT <= 512) ? 4 : (NT <= 64) ? 3 : 2;
-    static constexpr int PRE_INTS = KV_MAX_BATCH + 4;
+    static constexpr int PER_TILE = D / 4 + KV_TILE / 2 + NT;
+    static constexpr int BUFS = (4 * PER_TILE + NT <= 512) ? 4 : (3 * PER_TILE + NT <= 512) ? 3 : 2;
     // S^T runs up to BUFS tiles (so perhaps BUFS segments) ahead of the softmax, and Q two segments ahead of S^T
     static constexpr int ROWF_RING = 8;
     // page scales: the producer is up to STAGES tiles ahead of S^T, and that BUFS ahead of the softmax
     static constexpr int SCALE_RING = 16;
-    static constexpr int SMALL_BYTES = PRE_INTS * 4 + 2 * KV_MAX_BATCH    // tiles in front, rows, last tile's tokens
+    static constexpr int SMALL_BYTES = (KV_MAX_BATCH + 4) * 4 + 5 * KV_MAX_BATCH   // weight in front, tokens, rows
                                      + SCALE_RING * 8 * 8                 // page scales
                                      + ROWF_RING * NT * 4                 // row factors
                                      + 3 * NT * 4                         // -m, rescaling factors, sums
@@ -192,14 +250,16 @@ struct KvCfg {
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
     static_assert(ROWF_RING >= BUFS + 3 && SCALE_RING >= STAGES + BUFS, "rings");
     static constexpr int SMEM_BYTES = FIXED + STAGES * STAGE_BYTES;
-    static constexpr uint32_t IDESC_QK = (1u << 4) /*fp32*/ | ((uint32_t)(NT >> 3) << 17) | ((128u >> 4) << 24);   // E4M3 x E4M3
-    static constexpr uint32_t IDESC_PV = idesc_f16(0u /*f16*/, 128u, (uint32_t)NT) | (1u << 16);                   // B: rows fastest
+    // without the rows (bits 17 up: rows / 8)
+    static constexpr uint32_t IDESC_QK = (1u << 4) /*fp32*/ | ((128u >> 4) << 24);         // E4M3 x E4M3
+    static constexpr uint32_t IDESC_PV = idesc_f16(0u /*f16*/, 128u, 0u) | (1u << 16);     // B: rows fastest
     // P lies token by token, rows fastest (a softmax thread holds one token's rows): atoms of 8 tokens x 16 rows,
     // 32 bytes a token, 32-byte swizzle; the atoms of 8 tokens side by side, then the next 8 tokens
     static constexpr int P_ATOM = 256, P_STEP = (NT / 16) * P_ATOM;
-    // tensor memory columns: V tiles, S^T, one O^T
-    static constexpr int V_COL = 0, V_COLS = KV_TILE / 2;
-    static constexpr int S_COL = BUFS * V_COLS;
+    // tensor memory columns: K tiles, V tiles, S^T, one O^T
+    static constexpr int K_COL = 0, K_COLS = D / 4;
+    static constexpr int V_COL = BUFS * K_COLS, V_COLS = KV_TILE / 2;
+    static constexpr int S_COL = V_COL + BUFS * V_COLS;
     static constexpr int O_COL = S_COL + BUFS * NT;
     static constexpr int TMEM_COLS = 512;
     static_assert(O_COL + NT <= TMEM_COLS, "tensor memory budget");
@@ -309,38 +369,40 @@ __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile
     return false;
 }
 
-// Shared-memory matrix descriptor of a K-major operand without swizzle: 16-byte rows, 8 of them 128 contiguous bytes,
-// `rows8` bytes from one group of 8 rows to the next, `k16` bytes from one 16-byte step along the summed axis to the next.
-__device__ __forceinline__ uint64_t smem_desc_k_plain(uint32_t saddr, uint32_t rows8, uint32_t k16) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(k16 >> 4) << 16) | ((uint64_t)(rows8 >> 4) << 32) | ((uint64_t)1u << 46);
-}
-
-// D[tmem] (+)= A[smem] * B[smem], E4M3 operands, fp32 accumulate.
-__device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem], E4M3 operands, fp32 accumulate.
+__device__ __forceinline__ void mma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                   "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+
+// Eight values a lane -> over the warp's lanes, the combination of value 4 * (lane & 1) + (lane & 2) + (lane >> 2 & 1) in
+// every lane: three exchanges that halve the values, two that do not (nine shuffles against forty one by one).
+template <typename Op>
+__device__ __forceinline__ float kv_across8(float (&v)[8], int lane, Op op) {
+#pragma unroll
+    for (int w = 4, d = 1; w; w >>= 1, d <<= 1) {
+#pragma unroll
+        for (int j = 0; j < w; ++j) {
+            const bool hi = lane & d;
+            v[j] = op(hi ? v[j + w] : v[j], __shfl_xor_sync(0xFFFFFFFFu, hi ? v[j] : v[j + w], d));
+        }
+    }
+    v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 8));
+    return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 16));
 }
 
 __device__ __forceinline__ uint64_t kv_uniform64(uint64_t v) {
     return ((uint64_t)__shfl_sync(0xFFFFFFFFu, (uint32_t)(v >> 32), 0) << 32) | (uint64_t)__shfl_sync(0xFFFFFFFFu, (uint32_t)v, 0);
 }
-
-// A walk along a CTA's range that leaves out the units whose row tile holds no rows.
-struct KvWalk {
-    KvSegIter it;
-    const uint8_t* rows;      // rows of each request
-    int group, r0;            // query heads of a KV head; first row of this CTA's row tile
-    __device__ __forceinline__ KvWalk(const int* pre, const uint8_t* rows_, const KvAttnParams& p, long long begin, long long end, int r0_)
-        : it(pre, p.B, p.heads, begin, end), rows(rows_), group(p.group), r0(r0_) {}
-    __device__ __forceinline__ bool next(KvSeg& s) {
-        while (it.next(s))
-            if ((int)rows[s.b] * group > r0) return true;
-        return false;
-    }
-};
 
 // Ring position of a tile: buffer and parity of its use.
 template <int N>
@@ -356,20 +418,20 @@ struct KvRing {
 // swizzle). A non-finite element becomes NaN, and so does its row. By `threads` threads (a multiple of 32), in batches
 // of loads that are all in flight at once.
 template <int D, int NT, int BATCH>
-__device__ __forceinline__ void kv_load_rows(const KvAttnParams& p, const KvSeg& sg, int n_rows, int r0, int t, int threads, uint8_t* q_sm,
-                                             float* rowf) {
+__device__ __forceinline__ void kv_load_rows(const KvAttnParams& p, const KvSeg& sg, int t, int threads, uint8_t* q_sm, float* rowf) {
     constexpr int LPR = D / 8;                 // lanes of a row, 8 channels each
     const int first = p.row_start ? __ldg(p.row_start + sg.b) : sg.b * p.max_rows;
     const int c = t % LPR, step = threads / LPR;
     const unsigned inv_group = (65536u + p.group - 1) / p.group;     // r / group = r * inv_group >> 16 for r < 512, group <= 16
     const __nv_bfloat16* const q0 = p.q + (size_t)first * p.q_stride + (size_t)(sg.head * p.group) * D + 8 * c;
-    for (int n0 = t / LPR; n0 < NT; n0 += BATCH * step) {
+    const int r0 = sg.rt * sg.nt, nt = sg.nt;
+    for (int n0 = t / LPR; n0 < nt; n0 += BATCH * step) {
         uint4 q[BATCH];
 #pragma unroll
         for (int u = 0; u < BATCH; ++u) {
             const int n = n0 + u * step;
             q[u] = make_uint4(0, 0, 0, 0);
-            if (n < n_rows) {
+            if (n < sg.n_rows) {
                 const unsigned r = r0 + n, node = r * inv_group >> 16;
                 q[u] = __ldg(reinterpret_cast<const uint4*>(q0 + (size_t)node * p.q_stride + (size_t)(r - node * p.group) * D));
             }
@@ -387,7 +449,7 @@ __device__ __forceinline__ void kv_load_rows(const KvAttnParams& p, const KvSeg&
             }
 #pragma unroll
             for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-            if (n < NT) {
+            if (n < nt) {
                 // the smallest e with top <= 448 * 2^e: the significand's 7 bits behind the point against 1.75
                 const int e = max((int)(top >> 7) - 127, -100) - 8 + ((top & 0x7Fu) > 0x60u);
                 const float f = kv_pow2(-e);
@@ -424,8 +486,9 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     uint8_t* const stages = p_sm + BUFS * C::P_BYTES;
     uint64_t* const bars = reinterpret_cast<uint64_t*>(stages + C::STAGES * C::STAGE_BYTES);
     uint64_t* const kvfull = bars;               // [8] a stage's bytes and scales landed
-    uint64_t* const kvempty = kvfull + 8;        // [8] read by S^T and the converters
-    uint64_t* const qkdone = kvempty + 8;        // [4] S^T complete
+    uint64_t* const kvempty = kvfull + 8;        // [8] read by the movers
+    uint64_t* const kready = kvempty + 8;        // [4] K tile in tensor memory
+    uint64_t* const qkdone = kready + 4;         // [4] S^T complete (and the K tile free)
     uint64_t* const sempty = qkdone + 4;         // [4] S^T read by the softmax warps
     uint64_t* const vready = sempty + 4;         // [4] V tile in tensor memory
     uint64_t* const pready = vready + 4;         // [4] P in shared memory, O rescaled if need be
@@ -442,17 +505,17 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     float* const resc = negm + NT;                                                           // [NT]
     float* const lsum = resc + NT;                                                           // [NT]
     float* const red = lsum + NT;                                                            // [2][4][NH]
-    int* const pre = reinterpret_cast<int*>(red + 8 * NH);
-    uint8_t* const rows8 = reinterpret_cast<uint8_t*>(pre + C::PRE_INTS);
-    uint8_t* const last8 = rows8 + KV_MAX_BATCH;                                             // tokens of the last tile
+    unsigned* const pre = reinterpret_cast<unsigned*>(red + 8 * NH);                         // [B + 1]
+    int* const len_of = reinterpret_cast<int*>(pre + KV_MAX_BATCH + 4);                      // [B]
+    uint8_t* const rows8 = reinterpret_cast<uint8_t*>(len_of + KV_MAX_BATCH);                // [B]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the merge may be brought up now; it waits for this launch's parts by itself
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::STAGES; ++i) { mbar_init(&kvfull[i], 33); mbar_init(&kvempty[i], 5); }
+        for (int i = 0; i < C::STAGES; ++i) { mbar_init(&kvfull[i], 33); mbar_init(&kvempty[i], 4); }
         for (int i = 0; i < BUFS; ++i) {
-            mbar_init(&qkdone[i], 1); mbar_init(&sempty[i], 8);
+            mbar_init(&kready[i], 4); mbar_init(&qkdone[i], 1); mbar_init(&sempty[i], 8);
             mbar_init(&vready[i], 4); mbar_init(&pready[i], 8); mbar_init(&pvdone[i], 1);
         }
         for (int i = 0; i < 2; ++i) { mbar_init(&qready[i], 2); mbar_init(&qfree[i], 1); }
@@ -465,24 +528,23 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
         tmem_relinquish();
     }
     for (int b = threadIdx.x; b < p.B; b += C::THREADS) {
-        int first;
-        bool bad = false;
-        const int len = kv_len_of(p, b);
-        rows8[b] = (uint8_t)kv_rows_of(p, b, &first, &bad);
-        last8[b] = (uint8_t)(len - (kv_tiles(len) - 1) * KV_TILE);
-        pre[b + 1] = kv_tiles(len);
+        const KvRequest rq(p, b);
+        const KvShape sh(rq.rows * p.group, kv_tiles(rq.len), NT);
+        rows8[b] = (uint8_t)rq.rows;
+        len_of[b] = rq.len;
+        pre[b + 1] = rq.len > 0 ? (unsigned)(p.heads * sh.row_tiles) * sh.unit_w : 0u;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 0) {
-        // inclusive scan of the tiles
-        int carry = 0;
+        // inclusive scan of the weights
+        unsigned carry = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            int v = (b0 + lane < p.B) ? pre[b0 + lane + 1] : 0;
+            unsigned v = (b0 + lane < p.B) ? pre[b0 + lane + 1] : 0u;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+                const unsigned o = __shfl_up_sync(0xFFFFFFFFu, v, d);
                 if (lane >= d) v += o;
             }
             v += carry;
@@ -493,12 +555,9 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     }
     __syncthreads();
     const uint32_t tmem = *tmem_slot;
-    const long long total = (long long)p.heads * pre[p.B];
-    const long long groups = p.groups < total ? p.groups : total;
-    const int g = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
-    const long long t_begin = g < groups ? kv_range_start(g, total, groups) : 0;
-    const long long t_end = g < groups ? kv_range_start(g + 1, total, groups) : 0;
-    KvWalk walk(pre, rows8, p, t_begin, t_end, rt * NT);
+    const int g = blockIdx.x;
+    const KvShares shares(pre[p.B], p.ctas);
+    KvWalk walk(p, pre, len_of, rows8, shares.start(g), shares.start(g + 1), NT);
     KvSeg sg;
 
     if (warp < 4) {
@@ -507,7 +566,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             // ------------------------------------------------------------ producer
             const uint64_t pol = p.row_tiles > 1 ? policy_evict_normal() : policy_evict_first();
             const int per_tile = KV_TILE >> p.page_log2;
-            const uint32_t side_bytes = (uint32_t)D << p.page_log2, piece = 16u << p.page_log2;
+            const uint32_t page_bytes = 2u * D << p.page_log2;
             const uint32_t stage0 = smem_u32(stages);
             int s = 0;
             uint32_t ph = 0, issued = 0, last_ph = 0, tile = 0;
@@ -515,8 +574,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             int k = more ? sg.k0 : 0;
             // the page that this lane brings in of tile k: looked up a tile ahead
             auto look = [&](int& n) -> int {
-                const int len = (sg.tiles - 1) * KV_TILE + last8[sg.b];
-                n = min(((len + (1 << p.page_log2) - 1) >> p.page_log2) - k * per_tile, per_tile);
+                n = min((int)(((unsigned)len_of[sg.b] + (1u << p.page_log2) - 1) >> p.page_log2) - k * per_tile, per_tile);
                 return lane < n ? __ldg(p.table + (size_t)sg.b * p.width + (size_t)k * per_tile + lane) : 0;
             };
             int n = 0, id = more ? look(n) : 0;
@@ -536,20 +594,12 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                     if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_PRODUCER);
                     break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&kvfull[s], 2u * side_bytes * (uint32_t)cur_n);
+                if (lane == 0) mbar_arrive_expect_tx(&kvfull[s], page_bytes * (uint32_t)cur_n);
                 __syncwarp();
-                const uint32_t dst = stage0 + (uint32_t)(s * C::STAGE_BYTES);
-                const size_t unit = (size_t)page * p.heads + head;
-                for (int i0 = 0; i0 < cur_n * (D / 16); i0 += 32) {
-                    const int i = i0 + lane, j = i / (D / 16), c = i % (D / 16);
-                    const uint32_t u_lo = __shfl_sync(0xFFFFFFFFu, (uint32_t)unit, j & 31), u_hi = __shfl_sync(0xFFFFFFFFu, (uint32_t)(unit >> 32), j & 31);
-                    if (j < cur_n)
-                        bulk_load_s(dst + (uint32_t)c * (KV_TILE * 16) + (uint32_t)j * piece,
-                                    p.pages + (((size_t)u_hi << 32) | u_lo) * (2u * side_bytes) + (uint32_t)c * piece, piece, &kvfull[s], pol);
-                }
                 if (lane < cur_n) {
-                    bulk_load_s(dst + C::SIDE_BYTES + (uint32_t)lane * side_bytes, p.pages + unit * (2u * side_bytes) + side_bytes, side_bytes,
-                                &kvfull[s], pol);
+                    const size_t unit = (size_t)page * p.heads + head;
+                    bulk_load_s(stage0 + (uint32_t)(s * C::STAGE_BYTES) + page_bytes * (uint32_t)lane, p.pages + unit * page_bytes,
+                                page_bytes, &kvfull[s], pol);
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(page_scale + 8 * (tile % C::SCALE_RING) + lane)),
                                  "l"(p.scales + 2 * unit) : "memory");
                 }
@@ -567,7 +617,6 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
         } else if (warp < 3) {
             // ------------------------------------------------------------ MMA issuers
             const uint32_t tmem_u = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-            const uint64_t kdesc = kv_uniform64(smem_desc_k_plain(smem_u32(stages), 128u, KV_TILE * 16u));
             const uint64_t qdesc = kv_uniform64(smem_desc_k_sw128(smem_u32(q_sm)));
             const uint64_t pdesc = kv_uniform64(smem_desc_mn_sw32(smem_u32(p_sm), C::P_ATOM, C::P_STEP));
             const bool leader = elect_one();
@@ -579,28 +628,26 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 }
             };
             KvRing<BUFS> ring;
-            KvRing<C::STAGES> stage;
             uint32_t seg = 0;
             uint64_t* last_bar = nullptr;
             uint32_t last_par = 0;
             while (ok && walk.next(sg)) {
+                const uint32_t n_bits = (uint32_t)(sg.nt >> 3) << 17;
                 for (int k = sg.k0; k < sg.k1; ++k) {
                     const uint32_t b = ring.i;
                     if (warp == 1) {
                         if (k == sg.k0) wait(&qready[seg & 1u], (seg >> 1) & 1u);
-                        wait(&kvfull[stage.i], stage.par);
+                        wait(&kready[b], ring.par);
                         wait(&sempty[b], ring.par ^ 1u);
                         if (!ok) break;
                         tc_fence_after();
                         if (leader) {
-                            const uint64_t kd = kdesc + (uint64_t)(stage.i * (C::STAGE_BYTES >> 4));
                             const uint64_t qd = qdesc + (uint64_t)((seg & 1u) * (C::Q_BYTES >> 4));
-                            const uint32_t d = tmem_u + (uint32_t)(C::S_COL) + b * NT;
+                            const uint32_t d = tmem_u + (uint32_t)(C::S_COL) + b * NT, a = tmem_u + (uint32_t)C::K_COL + b * C::K_COLS;
 #pragma unroll
                             for (int i = 0; i < C::QSTEPS; ++i)
-                                mma_ss_f8(d, kd + (uint64_t)(((i % (D / 32)) * 2 * KV_TILE * 16) >> 4),
-                                          qd + (uint64_t)(((i >> 2) * NT * 128 + (i & 3) * 32) >> 4), C::IDESC_QK, i ? 1u : 0u);
-                            mma_commit(&kvempty[stage.i]);
+                                mma_ts_f8(d, a + 8u * (i % (D / 32)), qd + (uint64_t)(((i >> 2) * NT * 128 + (i & 3) * 32) >> 4),
+                                          C::IDESC_QK | n_bits, i ? 1u : 0u);
                             mma_commit(&qkdone[b]);
                             if (k + 1 == sg.k1) mma_commit(&qfree[seg & 1u]);
                         }
@@ -616,7 +663,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
 #pragma unroll
                             for (int i = 0; i < KV_TILE / 16; ++i)
                                 mma_ts_f16(tmem_u + (uint32_t)C::O_COL, tmem_u + (uint32_t)(C::V_COL + 8 * i) + b * C::V_COLS,
-                                           pd + (uint64_t)((2 * i * C::P_STEP) >> 4), C::IDESC_PV, (i || k != sg.k0) ? 1u : 0u);
+                                           pd + (uint64_t)((2 * i * C::P_STEP) >> 4), C::IDESC_PV | n_bits, (i || k != sg.k0) ? 1u : 0u);
                             mma_commit(&pvdone[b]);
                             if (k + 1 == sg.k1) mma_commit(ofull);
                         }
@@ -625,7 +672,6 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                     last_par = ring.par;
                     __syncwarp();
                     ring.step();
-                    stage.step();
                 }
                 ++seg;
             }
@@ -641,23 +687,23 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                         if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_PRODUCER);
                         break;
                     }
-                    kv_load_rows<D, NT, 5>(p, sg, min((int)rows8[sg.b] * p.group - rt * NT, NT), rt * NT, lane, 32,
-                                           q_sm + (seg & 1u) * C::Q_BYTES, rowf + (seg % C::ROWF_RING) * NT);
+                    kv_load_rows<D, NT, 5>(p, sg, lane, 32, q_sm + (seg & 1u) * C::Q_BYTES, rowf + (seg % C::ROWF_RING) * NT);
                     __syncwarp();
                     if (lane < 2) mbar_arrive(&qready[seg & 1u]);
                 }
                 ++seg;
             }
         }
-    } else if (warp < 12) {
-        // ------------------------------------------------------------ converters
-        regs_dec<C::REGS_CONVERT>();
-        const uint32_t set = (uint32_t)(warp - 4) >> 2;
-        const int qd = warp & 3, r = 32 * qd + lane;             // channel
+    } else if (warp < 8) {
+        // ------------------------------------------------------------ movers
+        regs_dec<C::REGS_MOVE>();
+        const int qd = warp & 3, r = 32 * qd + lane;             // token of the tile; channel
         const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16);
+        const int pl = p.page_log2;
+        const uint32_t page_bytes = 2u * D << pl;
+        const uint32_t k_off = (uint32_t)(r >> pl) * page_bytes + (uint32_t)(r & ((1 << pl) - 1)) * 16u;
         KvRing<C::STAGES> stage;
         KvRing<BUFS> ring;
-        uint32_t n = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             if (!__all_sync(0xFFFFFFFFu, kv_wait(bar, parity, abort_flag))) {
@@ -666,27 +712,36 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             }
         };
         while (ok && walk.next(sg)) {
-            for (int k = sg.k0; k < sg.k1; ++k, ++n, stage.step(), ring.step()) {
-                if ((n & 1u) != set) continue;
+            for (int k = sg.k0; k < sg.k1; ++k, stage.step(), ring.step()) {
                 const uint32_t b = ring.i;
                 wait(&kvfull[stage.i], stage.par);
                 if (!ok) break;
-                uint4 w[8];
-                if (D == 128 || qd < 2) {
-                    const uint8_t* const at = stages + stage.i * C::STAGE_BYTES + C::SIDE_BYTES + 16 * r;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4*>(at + 16 * D * c);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&kvempty[stage.i]);
-                // tokens behind the request's last one count nothing, whatever their bytes are
-                const int valid = (k + 1 == sg.tiles) ? last8[sg.b] : KV_TILE;
+                const uint8_t* const st = stages + stage.i * C::STAGE_BYTES;
                 uint32_t out[32];
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c)
+                    *reinterpret_cast<uint4*>(out + 4 * c) = *reinterpret_cast<const uint4*>(st + k_off + ((16u * c) << pl));
+                wait(&qkdone[b], ring.par ^ 1u);                  // the S^T that read this K buffer last
+                if (!ok) break;
+                tc_fence_after();
+                if (D == 128) tmem_st32(t_lane + (uint32_t)C::K_COL + b * C::K_COLS, out);
+                else tmem_st16(t_lane + (uint32_t)C::K_COL + b * C::K_COLS, out);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kready[b]);
+                // tokens behind the request's last one count nothing, whatever their bytes are
+                const int valid = (k + 1 == sg.tiles) ? walk.last(sg.b) : KV_TILE;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (D == 128 || qd < 2) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) kv_decode16(w[4 * half + c], out + 8 * c);
+                        for (int c = 0; c < 4; ++c) {
+                            const int t = 64 * half + 16 * c;
+                            kv_decode16(*reinterpret_cast<const uint4*>(st + (uint32_t)(t >> pl) * page_bytes + (uint32_t)(D << pl) +
+                                                                        (uint32_t)((t & ((1 << pl) - 1)) >> 4) * (16u * D) + 16u * r),
+                                        out + 8 * c);
+                        }
                         if (valid < KV_TILE) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) {
@@ -702,6 +757,9 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                         wait(&pvdone[b], ring.par ^ 1u);
                         if (!ok) break;
                         tc_fence_after();
+                    } else {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&kvempty[stage.i]);
                     }
                     if (D == 128 || qd < 2) tmem_st32(t_lane + (uint32_t)C::V_COL + b * C::V_COLS + 32u * half, out);
                 }
@@ -716,12 +774,15 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     } else {
         // ------------------------------------------------------------ softmax
         regs_inc<C::REGS_SOFTMAX>();
-        const int grp = (warp - 12) >> 2, qd = warp & 3, t = 32 * qd + lane;     // token of the tile; channel
-        const int c0 = grp * NH, bar_id = 1 + grp;
+        const int grp = (warp - 8) >> 2, qd = warp & 3, t = 32 * qd + lane;     // token of the tile; channel
+        const int c0 = 8 * grp, bar_id = 1 + grp;                                // block j of 8 rows begins at row 16 j + c0
         const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16);
         // this token's rows in P: 16-byte units of 8 rows, two a 32-byte line, swapped in every other four tokens
-        const uint32_t p_line = smem_u32(p_sm) + (uint32_t)((t >> 3) * C::P_STEP + (t & 7) * 32);
-        const uint32_t p_swap = (uint32_t)((t >> 2) & 1) << 4;
+        const uint32_t p_line = smem_u32(p_sm) + (uint32_t)((t >> 3) * C::P_STEP + (t & 7) * 32) + (((uint32_t)grp ^ ((t >> 2) & 1u)) << 4);
+        float* const g_negm = negm + grp * NH;        // this group's rows, block by block
+        float* const g_resc = resc + grp * NH;
+        float* const g_was = lsum + grp * NH;
+        float* const g_red = red + grp * 4 * NH;
         uint32_t n = 0, seg = 0;
         KvRing<BUFS> ring;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -730,12 +791,12 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_EPILOGUE);
         };
         while (walk.next(sg)) {
-            const int n_rows = min((int)rows8[sg.b] * p.group - rt * NT, NT);
             if (seg == 0) {
-                kv_load_rows<D, NT, 3>(p, sg, n_rows, rt * NT, (int)threadIdx.x - 384, 256, q_sm, rowf);
+                kv_load_rows<D, NT, 3>(p, sg, (int)threadIdx.x - 256, 256, q_sm, rowf);
                 kv_group_sync(bar_id);
                 if (t == 0) mbar_arrive(&qready[0]);
             }
+            const int nb = (sg.n_rows - c0 + 15) >> 4;               // blocks of this group that hold rows
             float l[NH];
 #pragma unroll
             for (int i = 0; i < NH; ++i) l[i] = 0.0f;
@@ -747,9 +808,10 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 tc_fence_after();
                 float x[NH];
 #pragma unroll
-                for (int i = 0; i < NH; i += 8) tmem_ld8(t_lane + (uint32_t)(C::S_COL + c0 + i) + b * NT, x + i);
+                for (int j = 0; j < C::NB; ++j)
+                    if (j < nb) tmem_ld8(t_lane + (uint32_t)(C::S_COL + 16 * j + c0) + b * NT, x + 8 * j);
                 const float2 sc = page_scale[8 * (n % C::SCALE_RING) + (t >> p.page_log2)];
-                const int valid = (k + 1 == sg.tiles) ? last8[sg.b] : KV_TILE;
+                const int valid = (k + 1 == sg.tiles) ? walk.last(sg.b) : KV_TILE;
                 const bool live = t < valid;
                 const float vs = live ? sc.y : 1.0f;
                 const float lv = kv_lg2(vs);
@@ -761,82 +823,88 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 // x = score - m
                 float top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < NH; i += 4) {
-                    const float4 rf = *reinterpret_cast<const float4*>(rowf + (seg % C::ROWF_RING) * NT + c0 + i);
-                    const float4 nm = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *reinterpret_cast<const float4*>(negm + c0 + i);
-                    f2_unpack(f2_fma(f2_mul(f2_pack(x[i], x[i + 1]), ks2), f2_pack(rf.x, rf.y), f2_pack(nm.x, nm.y)), x[i], x[i + 1]);
-                    f2_unpack(f2_fma(f2_mul(f2_pack(x[i + 2], x[i + 3]), ks2), f2_pack(rf.z, rf.w), f2_pack(nm.z, nm.w)), x[i + 2], x[i + 3]);
-                }
-                if (valid < KV_TILE) {
+                for (int j = 0; j < C::NB; ++j) {
+                    if (j < nb) {
 #pragma unroll
-                    for (int i = 0; i < NH; ++i) x[i] = live ? x[i] : -INFINITY;
-                }
+                        for (int i = 8 * j; i < 8 * j + 8; i += 4) {
+                            const float4 rf = *reinterpret_cast<const float4*>(rowf + (seg % C::ROWF_RING) * NT + 8 * j + c0 + i);
+                            const float4 nm = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *reinterpret_cast<const float4*>(g_negm + i);
+                            f2_unpack(f2_fma(f2_mul(f2_pack(x[i], x[i + 1]), ks2), f2_pack(rf.x, rf.y), f2_pack(nm.x, nm.y)), x[i], x[i + 1]);
+                            f2_unpack(f2_fma(f2_mul(f2_pack(x[i + 2], x[i + 3]), ks2), f2_pack(rf.z, rf.w), f2_pack(nm.z, nm.w)), x[i + 2], x[i + 3]);
+                        }
+                        if (valid < KV_TILE) {
 #pragma unroll
-                for (int i = 0; i < NH; ++i) top = fmaxf(top, x[i]);
+                            for (int i = 8 * j; i < 8 * j + 8; ++i) x[i] = live ? x[i] : -INFINITY;
+                        }
+#pragma unroll
+                        for (int i = 8 * j; i < 8 * j + 8; ++i) top = fmaxf(top, x[i]);
+                    }
+                }
                 if (kv_group_any(bar_id, first || top + lv > KV_SLACK)) {
                     // the reference moves: maxima of the log-weights over the tile's tokens
-                    float keep = -INFINITY, keep2 = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < NH; ++i) {
-                        const float nm = first ? 0.0f : negm[c0 + i];
-                        const float w = kv_warp_max(live ? (x[i] - nm) + lv : -INFINITY);
-                        if (i < 32) keep = (lane == i) ? w : keep;
-                        else keep2 = (lane == i - 32) ? w : keep2;
+                    for (int j = 0; j < C::NB; ++j) {
+                        if (j < nb) {
+                            float v[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[i] = live ? (x[8 * j + i] - (first ? 0.0f : g_negm[8 * j + i])) + lv : -INFINITY;
+                            const float w = kv_across8(v, lane, [](float a_, float b_) { return fmaxf(a_, b_); });
+                            if (lane < 8) g_red[qd * NH + 8 * j + ((lane & 1) << 2) + (lane & 2) + (lane >> 2)] = w;
+                        }
                     }
-                    if (lane < NH) red[(grp * 4 + qd) * NH + lane] = keep;
-                    if (NH > 32 && lane < NH - 32) red[(grp * 4 + qd) * NH + 32 + lane] = keep2;
                     kv_group_sync(bar_id);
-                    if (t < NH) {
-                        const float* const rd = red + grp * 4 * NH + t;
-                        const float old = first ? -INFINITY : -negm[c0 + t];
+                    if (t < 8 * nb) {
+                        const float* const rd = g_red + t;
+                        const float old = first ? -INFINITY : -g_negm[t];
                         const float now = fmaxf(old, fmaxf(fmaxf(rd[0], rd[NH]), fmaxf(rd[2 * NH], rd[3 * NH])));
                         // what x is off by, and what O and l shrink by (nothing is held yet under an old m of minus infinity)
-                        resc[c0 + t] = (old == -INFINITY) ? 0.0f : kv_ex2(old - now);
-                        lsum[c0 + t] = first ? 0.0f : negm[c0 + t];
-                        negm[c0 + t] = -now;
+                        g_resc[t] = (old == -INFINITY) ? 0.0f : kv_ex2(old - now);
+                        g_was[t] = first ? 0.0f : g_negm[t];
+                        g_negm[t] = -now;
                     }
                     kv_group_sync(bar_id);
                     if (!first) wait(&pvdone[was_b], was_par);    // O holds every tile before this one
                     tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < NH; i += 8) {
-                        float o[8];
-                        if (!first) {
-                            tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0 + i), o);
-                            tmem_wait_ld();
-                        }
+                    for (int j = 0; j < C::NB; ++j) {
+                        if (j < nb) {
+                            float o[8];
+                            if (!first) {
+                                tmem_ld8(t_lane + (uint32_t)(C::O_COL + 16 * j + c0), o);
+                                tmem_wait_ld();
+                            }
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float f = resc[c0 + i + j];
-                            x[i + j] = (x[i + j] - lsum[c0 + i + j]) + negm[c0 + i + j];
-                            l[i + j] *= f;
-                            o[j] *= f;
+                            for (int i = 0; i < 8; ++i) {
+                                const float f = g_resc[8 * j + i];
+                                x[8 * j + i] = (x[8 * j + i] - g_was[8 * j + i]) + g_negm[8 * j + i];
+                                if (valid < KV_TILE) x[8 * j + i] = live ? x[8 * j + i] : -INFINITY;
+                                l[8 * j + i] *= f;
+                                o[i] *= f;
+                            }
+                            if (!first) tmem_st8(t_lane + (uint32_t)(C::O_COL + 16 * j + c0), o);
                         }
-                        if (!first) tmem_st8(t_lane + (uint32_t)(C::O_COL + c0 + i), o);
                     }
                     if (!first) tmem_wait_st();
-                    if (valid < KV_TILE) {
-#pragma unroll
-                        for (int i = 0; i < NH; ++i) x[i] = live ? x[i] : -INFINITY;
-                    }
                 }
                 wait(&pvdone[b], ring.par ^ 1u);                  // the O^T that read this P buffer last
                 const float vs8 = vs * 256.0f;                    // 2^KV_P_SHIFT
                 const uint64_t vs2 = f2_pack(vs8, vs8);
                 const uint32_t at = p_line + b * C::P_BYTES;
 #pragma unroll
-                for (int i = 0; i < NH; i += 8) {
-                    uint32_t h[4];
+                for (int j = 0; j < C::NB; ++j) {
+                    if (j < nb) {
+                        uint32_t h[4];
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const uint64_t e2 = f2_pack(kv_ex2(x[i + j]), kv_ex2(x[i + j + 1]));
-                        f2_unpack(f2_add(f2_pack(l[i + j], l[i + j + 1]), e2), l[i + j], l[i + j + 1]);
-                        float w0, w1;
-                        f2_unpack(f2_mul(e2, vs2), w0, w1);
-                        h[j >> 1] = kv_pack_f16(w0, w1);
+                        for (int i = 0; i < 8; i += 2) {
+                            const int c = 8 * j + i;
+                            const uint64_t e2 = f2_pack(kv_ex2(x[c]), kv_ex2(x[c + 1]));
+                            f2_unpack(f2_add(f2_pack(l[c], l[c + 1]), e2), l[c], l[c + 1]);
+                            float w0, w1;
+                            f2_unpack(f2_mul(e2, vs2), w0, w1);
+                            h[i >> 1] = kv_pack_f16(w0, w1);
+                        }
+                        sts_128(at + j * C::P_ATOM, h[0], h[1], h[2], h[3]);
                     }
-                    const uint32_t u = (uint32_t)(c0 + i) >> 3;   // unit of 8 rows
-                    sts_128(at + (u >> 1) * C::P_ATOM + (((u & 1u) << 4) ^ p_swap), h[0], h[1], h[2], h[3]);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -847,43 +915,39 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 ++n;
                 ring.step();
             }
-            // the segment's part: l over the lanes (eight rows at a time: three exchanges leave a lane one row) and
-            // warps, O as it lies
+            // the segment's part: l over the lanes and warps, O as it lies
 #pragma unroll
-            for (int i = 0; i < NH; i += 8) {
-                float v[8];
+            for (int j = 0; j < C::NB; ++j) {
+                if (j < nb) {
+                    float v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = l[i + j];
-#pragma unroll
-                for (int w = 4, d = 1; w; w >>= 1, d <<= 1) {
-#pragma unroll
-                    for (int j = 0; j < w; ++j) {
-                        const bool hi = lane & d;
-                        const float mine = hi ? v[j + w] : v[j], other = hi ? v[j] : v[j + w];
-                        v[j] = mine + __shfl_xor_sync(0xFFFFFFFFu, other, d);
-                    }
+                    for (int i = 0; i < 8; ++i) v[i] = l[8 * j + i];
+                    const float w = kv_across8(v, lane, [](float a_, float b_) { return a_ + b_; });
+                    if (lane < 8) g_red[qd * NH + 8 * j + ((lane & 1) << 2) + (lane & 2) + (lane >> 2)] = w;
                 }
-                v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 8);
-                v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);
-                if (lane < 8) red[(grp * 4 + qd) * NH + i + ((lane & 1) << 2) + (lane & 2) + (lane >> 2)] = v[0];
             }
-            const size_t slot = (((size_t)sg.b * p.heads + sg.head + g) * p.row_tiles + rt) * NT;
+            const size_t slot = (((size_t)sg.b * p.heads + sg.head) * p.row_tiles + sg.rt + g) * NT;
             kv_group_sync(bar_id);
-            if (t < NH && c0 + t < n_rows) {
-                const float* const rd = red + grp * 4 * NH + t;
-                p.part_ml[slot + c0 + t] = make_float2(-negm[c0 + t] - KV_P_SHIFT, 256.0f * ((rd[0] + rd[NH]) + (rd[2 * NH] + rd[3 * NH])));
+            {
+                const int row = 16 * (t >> 3) + c0 + (t & 7);
+                if (t < 8 * nb && row < sg.n_rows) {
+                    const float* const rd = g_red + t;
+                    p.part_ml[slot + row] = make_float2(-g_negm[t] - KV_P_SHIFT, 256.0f * ((rd[0] + rd[NH]) + (rd[2 * NH] + rd[3 * NH])));
+                }
             }
             wait(ofull, seg & 1u);
             tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < NH; i += 8) {
-                float o[8];
-                tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0 + i), o);
-                tmem_wait_ld();
-                if (D == 128 || qd < 2) {
+            for (int j = 0; j < C::NB; ++j) {
+                if (j < nb) {
+                    float o[8];
+                    tmem_ld8(t_lane + (uint32_t)(C::O_COL + 16 * j + c0), o);
+                    tmem_wait_ld();
+                    if (D == 128 || qd < 2) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (c0 + i + j < n_rows) p.part_o[(slot + c0 + i + j) * D + t] = o[j];
+                        for (int i = 0; i < 8; ++i)
+                            if (16 * j + c0 + i < sg.n_rows) p.part_o[(slot + 16 * j + c0 + i) * D + t] = o[i];
+                    }
                 }
             }
             tc_fence_before();
@@ -913,14 +977,17 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
     constexpr int E = D / 32;                            // channels of a lane
     constexpr int RP = D + 8;                            // padded row: 16-byte reads of eight rows spread over the banks
     __shared__ __align__(16) __nv_bfloat16 kn[KV_MAX_ROWS * RP], vn[KV_MAX_ROWS * RP];
-    __shared__ long long sums[2][KV_MERGE_WARPS];
+    __shared__ unsigned sums[2][KV_MERGE_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x, head = blockIdx.y / chunks, chunk = blockIdx.y % chunks;
-    int first;
-    bool bad = false;
-    const int rows = kv_rows_of(p, b, &first, &bad);
-    if (bad && tid == 0 && blockIdx.y == 0) atomicCAS(p.err, 0, TL_DEV_ERR_KV_ROWS);
-    if (chunk * KV_MERGE_WARPS >= rows * p.group) return;
+    const KvRequest rq(p, b);
+    const int first = rq.first, rows = rq.rows;
+    if (rq.bad && tid == 0 && blockIdx.y == 0) atomicCAS(p.err, 0, TL_DEV_ERR_KV_ROWS);
+    // every CTA waits for the streaming kernel, so that this launch never ends before it
+    if (chunk * KV_MERGE_WARPS >= rows * p.group) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     if (p.k_new) {
         for (int e = tid; e < rows * (D / 8); e += KV_MERGE_THREADS) {
             const int j = e / (D / 8), c = e % (D / 8);
@@ -930,24 +997,26 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
         }
     }
     // this request's place in the tile list
-    long long before = 0, all = 0;
+    unsigned before = 0, all = 0;
     for (int i = tid; i < p.B; i += KV_MERGE_THREADS) {
-        const int n = kv_tiles(kv_len_of(p, i));
-        all += n;
-        if (i < b) before += n;
+        const KvRequest other(p, i);
+        const KvShape sh(other.rows * p.group, kv_tiles(other.len), p.nt);
+        const unsigned w = other.len > 0 ? (unsigned)(p.heads * sh.row_tiles) * sh.unit_w : 0u;
+        all += w;
+        if (i < b) before += w;
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
-        before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
-    }
+    all = __reduce_add_sync(0xFFFFFFFFu, all);
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
     if (lane == 0) { sums[0][warp] = all; sums[1][warp] = before; }
     __syncthreads();
     all = before = 0;
 #pragma unroll
     for (int u = 0; u < KV_MERGE_WARPS; ++u) { all += sums[0][u]; before += sums[1][u]; }
     const int r = chunk * KV_MERGE_WARPS + warp;
-    if (r >= rows * p.group) return;
+    if (r >= rows * p.group) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     const int i = r / p.group, h = head * p.group + r % p.group;
     const int row = first + i;
 
@@ -990,37 +1059,59 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
             }
         }
     }
-    // the parts of the cached tokens
-    const int len = kv_len_of(p, b);
+    // the parts of the cached tokens: a lane looks at a part (whether the CTA had a tile of the unit, and its m and l), then
+    // all lanes add the parts' O in order, eight loads in flight
+    const int tiles = kv_tiles(rq.len);
+    const KvShape sh(rows * p.group, tiles, p.nt);
+    const int rt = r / sh.nt, n = r - rt * sh.nt;
+    const unsigned at0 = before + (unsigned)(head * sh.row_tiles + rt) * sh.unit_w;
+    const long long slot0 = ((long long)b * p.heads + head) * p.row_tiles + rt;
+    const KvShares shares(all, p.ctas);
+    int g0 = 0, g1 = -1;
+    if (rq.len > 0) {
+        g0 = shares.owner(at0);
+        g1 = shares.owner(at0 + sh.unit_w - 1);
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (len > 0) {
-        const int tiles = kv_tiles(len);
-        const long long total = (long long)p.heads * all, groups = p.groups < total ? p.groups : total;
-        const long long a = (long long)p.heads * before + (long long)head * tiles, z = a + tiles;
-        const int g0 = (int)(((a + 1) * groups - 1) / total), g1 = (int)((z * groups - 1) / total);
-        const int rt = r / p.nt, n = r % p.nt;
-        // four parts' loads in flight at once
-        for (int g = g0; g <= g1; g += 4) {
-            float2 ml[4], x[4][E / 2];
+    for (int gb = g0; gb <= g1; gb += 32) {
+        const int g = gb + lane;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        bool has = false;
+        if (g <= g1) {
+            const unsigned lo = shares.start(g), hi = shares.start(g + 1);
+            has = sh.tile_from(lo > at0 ? lo - at0 : 0u, tiles) < sh.tile_from(hi > at0 ? hi - at0 : 0u, tiles);
+            if (has) ml = __ldcg(p.part_ml + (size_t)(slot0 + g) * p.nt + n);
+        }
+        const float top = fmaxf(m, kv_warp_max(ml.x));
+        // a part or tree without weight (m of minus infinity) counts nothing, but a NaN of it counts
+        const float f0 = (m == -INFINITY) ? 0.0f : exp2f(m - top), f = (ml.x == -INFINITY) ? 0.0f : exp2f(ml.x - top);
+        float sum = ml.y * f;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const size_t at = (((size_t)b * p.heads + head + min(g + u, g1)) * p.row_tiles + rt) * p.nt + n;
-                ml[u] = (g + u <= g1) ? __ldcg(p.part_ml + at) : make_float2(-INFINITY, 0.0f);
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        m = top;
+        l = l * f0 + sum;
 #pragma unroll
-                for (int e = 0; e < E; e += 2) x[u][e / 2] = __ldcg(reinterpret_cast<const float2*>(p.part_o + at * D + E * lane + e));
+        for (int e = 0; e < E; ++e) o[e] *= f0;
+        unsigned todo = __ballot_sync(0xFFFFFFFFu, has);
+        while (todo) {
+            float2 x[8][E / 2];
+            float fs[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int src = todo ? __ffs(todo) - 1 : 0;
+                fs[u] = todo ? __shfl_sync(0xFFFFFFFFu, f, src) : 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    x[u][e / 2] = todo ? __ldcg(reinterpret_cast<const float2*>(p.part_o + ((size_t)(slot0 + gb + src) * p.nt + n) * D + E * lane + e))
+                                       : make_float2(0.0f, 0.0f);
+                todo &= todo - 1;
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (g + u > g1) break;
-                const float top = fmaxf(m, ml[u].x);
-                // a part or tree without weight (m of minus infinity) counts nothing
-                const float f0 = (m == -INFINITY) ? 0.0f : exp2f(m - top), f1 = (ml[u].x == -INFINITY) ? 0.0f : exp2f(ml[u].x - top);
-                m = top;
-                l = l * f0 + ml[u].y * f1;
+            for (int u = 0; u < 8; ++u) {
 #pragma unroll
                 for (int e = 0; e < E; e += 2) {
-                    o[e] = o[e] * f0 + x[u][e / 2].x * f1;
-                    o[e + 1] = o[e + 1] * f0 + x[u][e / 2].y * f1;
+                    o[e] = fmaf(x[u][e / 2].x, fs[u], o[e]);
+                    o[e + 1] = fmaf(x[u][e / 2].y, fs[u], o[e + 1]);
                 }
             }
         }

@@ -1254,22 +1254,20 @@ size_t strided_bytes(int rows, long long stride, size_t width) {
     return rows > 0 ? ((size_t)(rows - 1) * (size_t)stride + width) * 2 : 0;
 }
 
-// How an attention call's rows are cut: `nt` rows a tile, `row_tiles` tiles a unit, the parts that can
-// arise on `ctas` CTAs, and the bytes they take.
+// How an attention call's rows are cut: row tiles of at most `nt` rows, `row_tiles` of them for a request with the most
+// rows (fewer rows are cut on the device, KvShape), and the bytes of the parts that can arise on kKvMaxCtas CTAs.
 constexpr int kKvMaxCtas = 160;   // CTAs of the streaming kernel at most (a B200 has 148 SMs)
 struct KvSplit {
-    int nt, row_tiles, groups;
+    int nt, row_tiles;
     size_t o_bytes, ml_bytes;
 };
-KvSplit kv_split(const tl_kv_cache& c, int n_q_heads, int B, int max_rows, int ctas) {
+KvSplit kv_split(const tl_kv_cache& c, int n_q_heads, int B, int max_rows) {
     KvSplit s;
     const int rows = max_rows * (n_q_heads / c.n_kv_heads);
-    // the fewest row tiles of at most 80 rows (tensor memory holds no more beside two K and two V tiles), and the
-    // rows dealt out evenly over them in steps of 16, the MMA's
+    // the fewest row tiles of at most 80 rows (tensor memory holds no more beside two K, V and S tiles), in steps of 16, the MMA's
     s.row_tiles = (rows + 79) / 80;
     s.nt = ((rows + s.row_tiles - 1) / s.row_tiles + 15) / 16 * 16;
-    s.groups = ctas / s.row_tiles;
-    const size_t parts = ((size_t)B * c.n_kv_heads + kKvMaxCtas) * s.row_tiles * s.nt;
+    const size_t parts = ((size_t)B * c.n_kv_heads * s.row_tiles + kKvMaxCtas) * s.nt;
     s.o_bytes = parts * c.head_dim * sizeof(float);
     s.ml_bytes = parts * sizeof(float2);
     return s;
@@ -1300,7 +1298,7 @@ template <int D, int NT>
 tl_status launch_kv_stream(const tl::KvAttnParams& p, cudaStream_t stream) {
     using C = tl::KvCfg<D, NT>;
     TL_CUDA(cudaFuncSetAttribute(tl::kv_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES));
-    tl::kv_attention_kernel<D, NT><<<(unsigned)(p.groups * p.row_tiles), C::THREADS, C::SMEM_BYTES, stream>>>(p);
+    tl::kv_attention_kernel<D, NT><<<(unsigned)p.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(p);
     TL_CUDA(cudaGetLastError());
     return TL_OK;
 }
@@ -1741,7 +1739,7 @@ tl_status tl_kv_attention_workspace(const tl_kv_cache* cache, int n_q_heads, int
     if (!bytes) return fail(TL_ERR_INVALID_VALUE, "null pointer");
     st = check_kv_heads(*cache, n_q_heads, B, max_rows);
     if (st != TL_OK) return st;
-    const KvSplit s = kv_split(*cache, n_q_heads, B, max_rows, kKvMaxCtas);
+    const KvSplit s = kv_split(*cache, n_q_heads, B, max_rows);
     *bytes = s.o_bytes + s.ml_bytes;
     return TL_OK;
 }
@@ -1758,6 +1756,13 @@ tl_status tl_kv_attention(const void* q, long long q_stride, int n_q_heads, cons
     const size_t qw = (size_t)n_q_heads * cache->head_dim, nw = (size_t)cache->n_kv_heads * cache->head_dim;
     if (table_width < 1 || (long long)table_width * cache->page_tokens > 0x3FFFFFFFll)
         return fail(TL_ERR_INVALID_VALUE, "table_width = %d: need 1 or more and at most 2^30 tokens", table_width);
+    // the device adds up the work of a call (tiles of 128 tokens, each of a weight up to 9, per head and row tile) in 32 bits
+    {
+        const long long tiles = ((long long)table_width * cache->page_tokens + 127) / 128;
+        const int row_tiles = (max_rows * (n_q_heads / cache->n_kv_heads) + 79) / 80;
+        if ((double)B * cache->n_kv_heads * row_tiles * (12.0 + 9.0 * (double)tiles) > 4.0e9)
+            return fail(TL_ERR_UNSUPPORTED, "B * n_kv_heads * table_width is too large for one call: give fewer requests");
+    }
     if (R < 0 || (!row_start && R != B * max_rows))
         return fail(TL_ERR_INVALID_VALUE, "R = %d: without row_start it is B * max_rows = %d", R, B * max_rows);
     if (R == 0) return TL_OK;
@@ -1773,9 +1778,9 @@ tl_status tl_kv_attention(const void* q, long long q_stride, int n_q_heads, cons
     if (q_stride < (long long)qw || q_stride % 8 || out_stride < (long long)qw || out_stride % 8 ||
         (k_new && (new_stride < (long long)nw || new_stride % 8)))
         return fail(TL_ERR_INVALID_VALUE, "strides must be multiples of 8 that hold a row (%zu, %zu elements)", qw, nw);
-    const KvSplit most = kv_split(*cache, n_q_heads, B, max_rows, kKvMaxCtas);
-    if (workspace_bytes < most.o_bytes + most.ml_bytes)
-        return fail(TL_ERR_INVALID_VALUE, "workspace of %zu bytes: %zu are needed", workspace_bytes, most.o_bytes + most.ml_bytes);
+    const KvSplit sp = kv_split(*cache, n_q_heads, B, max_rows);
+    if (workspace_bytes < sp.o_bytes + sp.ml_bytes)
+        return fail(TL_ERR_INVALID_VALUE, "workspace of %zu bytes: %zu are needed", workspace_bytes, sp.o_bytes + sp.ml_bytes);
     {
         const size_t nb = strided_bytes(R, new_stride, nw);
         const void* at[10] = {out, workspace, q, cache->pages, cache->scales, table, lens, row_start, mask, k_new};
@@ -1793,7 +1798,6 @@ tl_status tl_kv_attention(const void* q, long long q_stride, int n_q_heads, cons
     DevState* d = nullptr;
     st = current_state(&d);
     if (st != TL_OK) return st;
-    const KvSplit sp = kv_split(*cache, n_q_heads, B, max_rows, d->num_sms < kKvMaxCtas ? d->num_sms : kKvMaxCtas);
     tl::KvAttnParams p;
     memset(&p, 0, sizeof p);
     p.q = static_cast<const __nv_bfloat16*>(q);
@@ -1821,7 +1825,7 @@ tl_status tl_kv_attention(const void* q, long long q_stride, int n_q_heads, cons
     p.group = n_q_heads / cache->n_kv_heads;
     p.R = R;
     p.max_rows = max_rows;
-    p.groups = sp.groups;
+    p.ctas = d->num_sms < kKvMaxCtas ? d->num_sms : kKvMaxCtas;
     p.row_tiles = sp.row_tiles;
     p.nt = sp.nt;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
