@@ -113,8 +113,9 @@ struct KvShares {
 };
 
 // One step of a walk along a range of the tile list: tiles k0..k1 of row tile rt of (b, head).
-struct KvSeg {
-    int b, head, rt, k0, k1, tiles, nt, n_rows;
+struct __align__(16) KvSeg {
+    int b, head, rt, k0, k1, nt, n_rows;
+    int valid;      // tokens of its last tile (128 unless it is the unit's last)
 };
 
 struct KvWalk {
@@ -137,6 +138,7 @@ struct KvWalk {
           tiles(0), at(0) {
         if (begin >= end) return;
         int lo = 0, hi = B;
+#pragma unroll 1
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (pre[mid] <= begin) lo = mid; else hi = mid;
@@ -158,7 +160,9 @@ struct KvWalk {
         rt = 0;
         if (++head < heads) return;
         head = 0;
-        do ++b; while (b < B && pre[b + 1] == pre[b]);
+        ++b;
+#pragma unroll 1
+        while (b < B && pre[b + 1] == pre[b]) ++b;
         if (b < B) look();
     }
     __device__ __forceinline__ bool next(KvSeg& g) {
@@ -170,15 +174,13 @@ struct KvWalk {
         g.rt = rt;
         g.k0 = k;
         g.k1 = k1;
-        g.tiles = tiles;
         g.nt = s.nt;
         g.n_rows = min((int)rows[b] * group - rt * s.nt, s.nt);
+        g.valid = k1 == tiles ? ((len[b] - 1) & (KV_TILE - 1)) + 1 : KV_TILE;
         k = k1;
         if (k == tiles) step();
         return true;
     }
-    // tokens of the last tile of request b_
-    __device__ __forceinline__ int last(int b_) const { return ((len[b_] - 1) & (KV_TILE - 1)) + 1; }
 };
 
 // ---------------------------------------------------------------- the streaming kernel
@@ -204,7 +206,9 @@ struct KvWalk {
 // l rescaled. So most tiles need one comparison a score and one vote.
 //
 // Roles (one CTA of 16 warps per SM; registers are moved between the warpgroups, KvCfg):
-//   * warp 0        producer: a page's K and V of the head are one contiguous piece, brought in by one bulk copy;
+//   * warp 0        walks the CTA's share of the list and publishes its segments (a unit's tiles, KvSeg) in a ring that the
+//                   other roles follow (the walk in every role was code of 8 KB each, and instruction fetches a bound);
+//                   producer: a page's K and V of the head are one contiguous piece, brought in by one bulk copy;
 //                   tiles of 128 tokens, a ring of stages. Scales follow by cp.async.
 //   * warp 1        issues the MMAs of S^T, warp 2 those of O^T (an issuer manages one MMA in some 55 cycles while
 //                   other warps run, so one warp for all sixteen of a tile was a bound).
@@ -239,12 +243,14 @@ struct KvCfg {
     static constexpr int ROWF_RING = 8;
     // page scales: the producer is up to STAGES tiles ahead of S^T, and that BUFS ahead of the softmax
     static constexpr int SCALE_RING = 16;
+    static constexpr int SEG_RING = 16;
     static constexpr int SMALL_BYTES = (KV_MAX_BATCH + 4) * 4 + 5 * KV_MAX_BATCH   // weight in front, tokens, rows
                                      + SCALE_RING * 8 * 8                 // page scales
                                      + ROWF_RING * NT * 4                 // row factors
-                                     + 3 * NT * 4                         // -m, rescaling factors, sums
+                                     + 2 * NT * 4                         // -m, rescaling factors
                                      + 2 * 4 * NH * 4                     // a group's four warps' maxima or sums
-                                     + 512;                               // barriers
+                                     + SEG_RING * 32                      // segments
+                                     + 768;                               // barriers
     static constexpr int FIXED = 2 * Q_BYTES + BUFS * P_BYTES + SMALL_BYTES + 1024 /*align*/;
     static constexpr int FIT = (232448 - FIXED) / STAGE_BYTES;
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
@@ -362,11 +368,17 @@ __device__ __forceinline__ void kv_decode16(uint4 q, uint32_t* out) {
 // Bounded wait that also gives up when another role has aborted the CTA. A poll may sleep in hardware for some 20
 // microseconds: the limit is seconds, far beyond any launch.
 __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+#pragma unroll 1
     for (uint32_t i = 0; i < (TL_WAIT_LIMIT >> 4); ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 15u) == 15u && *abort_flag) return false;
     }
     return false;
+}
+
+// The first n bytes of a word (none for n <= 0), zeros behind them.
+__device__ __forceinline__ uint32_t kv_first_bytes(uint32_t w, int n) {
+    return n >= 4 ? w : n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u);
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], E4M3 operands, fp32 accumulate.
@@ -400,6 +412,14 @@ __device__ __forceinline__ float kv_across8(float (&v)[8], int lane, Op op) {
     return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 16));
 }
 
+// Bounded wait that does not mind an abort: for work in flight that has to end before the CTA may.
+__device__ __forceinline__ bool kv_drain(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < (TL_WAIT_LIMIT >> 4); ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return false;
+}
+
 __device__ __forceinline__ uint64_t kv_uniform64(uint64_t v) {
     return ((uint64_t)__shfl_sync(0xFFFFFFFFu, (uint32_t)(v >> 32), 0) << 32) | (uint64_t)__shfl_sync(0xFFFFFFFFu, (uint32_t)v, 0);
 }
@@ -415,9 +435,10 @@ struct KvRing {
 
 // The Q rows of a segment's row tile into shared memory as two E4M3 terms, each row scaled by a power of two; rowf[n]
 // undoes the scale. D = 128: a slab of 128-byte rows for each term; D = 64: one slab, both terms side by side (128-byte
-// swizzle). A non-finite element becomes NaN, and so does its row. By `threads` threads (a multiple of 32), in batches
-// of loads that are all in flight at once.
-template <int D, int NT, int BATCH>
+// swizzle). A row with a non-finite element gets a NaN factor. By `threads` threads (a multiple of 32): the bf16 rows
+// are first copied, all at once, to where their terms will lie (a row's 2 D bytes are as many as its terms'); then
+// the lanes of a row read all of it and write it back as terms.
+template <int D, int NT>
 __device__ __forceinline__ void kv_load_rows(const KvAttnParams& p, const KvSeg& sg, int t, int threads, uint8_t* q_sm, float* rowf) {
     constexpr int LPR = D / 8;                 // lanes of a row, 8 channels each
     const int first = p.row_start ? __ldg(p.row_start + sg.b) : sg.b * p.max_rows;
@@ -425,51 +446,48 @@ __device__ __forceinline__ void kv_load_rows(const KvAttnParams& p, const KvSeg&
     const unsigned inv_group = (65536u + p.group - 1) / p.group;     // r / group = r * inv_group >> 16 for r < 512, group <= 16
     const __nv_bfloat16* const q0 = p.q + (size_t)first * p.q_stride + (size_t)(sg.head * p.group) * D + 8 * c;
     const int r0 = sg.rt * sg.nt, nt = sg.nt;
-    for (int n0 = t / LPR; n0 < nt; n0 += BATCH * step) {
-        uint4 q[BATCH];
+    // 16-byte unit of the row that this lane copies; for D = 128 the second half of a row lies in the second slab
+    const uint32_t unit = c & 7, slab = (uint32_t)(c >> 3) * (NT * 128);
+#pragma unroll 1
+    for (int n = t / LPR; n < nt; n += step) {
+        const unsigned r = r0 + n, node = r * inv_group >> 16;
+        const bool there = n < sg.n_rows;
+        const __nv_bfloat16* const from = there ? q0 + (size_t)node * p.q_stride + (size_t)(r - node * p.group) * D : p.q;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(q_sm + slab + n * 128 + (unit << 4))), "l"(from),
+                     "r"(there ? 16 : 0) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    const int c2 = (D == 128) ? c : c + 8;
+    const uint32_t slab2 = (D == 128) ? NT * 128 : 0;
+    // nt is a multiple of 16 and a warp's rows are a power of two up to 8: whole warps leave the loop together
+#pragma unroll 1
+    for (int n = t / LPR; n < nt; n += step) {
+        const uint4 q = *reinterpret_cast<const uint4*>(q_sm + slab + n * 128 + (unit << 4));    // this lane's own copy
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        uint32_t m = 0;
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
-            const int n = n0 + u * step;
-            q[u] = make_uint4(0, 0, 0, 0);
-            if (n < sg.n_rows) {
-                const unsigned r = r0 + n, node = r * inv_group >> 16;
-                q[u] = __ldg(reinterpret_cast<const uint4*>(q0 + (size_t)node * p.q_stride + (size_t)(r - node * p.group) * D));
-            }
+        for (int v = 0; v < 4; ++v) m = __vmaxu2(m, w[v] & 0x7FFF7FFFu);
+        unsigned top = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+        for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        // the smallest e with top <= 448 * 2^e: the significand's 7 bits behind the point against 1.75
+        const int e = max((int)(top >> 7) - 127, -100) - 8 + ((top & 0x7Fu) > 0x60u);
+        const float f = kv_pow2(-e);
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const float x = __int_as_float((int)(w[v] << 16)) * f, y = __int_as_float((int)(w[v] & 0xFFFF0000u)) * f;
+            const uint32_t a = kv_e4m3x2(x, y), h = kv_f16x2(a);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            const uint32_t b = kv_e4m3x2(x - back.x, y - back.y);
+            hi[v >> 1] = (v & 1) ? (hi[v >> 1] | (a << 16)) : a;
+            lo[v >> 1] = (v & 1) ? (lo[v >> 1] | (b << 16)) : b;
         }
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
-            const int n = n0 + u * step;
-            const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-            unsigned top = 0;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const unsigned lo = w[v] & 0x7FFFu, hi = (w[v] >> 16) & 0x7FFFu;
-                if (lo < 0x7F80u) top = max(top, lo);
-                if (hi < 0x7F80u) top = max(top, hi);
-            }
-#pragma unroll
-            for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-            if (n < nt) {
-                // the smallest e with top <= 448 * 2^e: the significand's 7 bits behind the point against 1.75
-                const int e = max((int)(top >> 7) - 127, -100) - 8 + ((top & 0x7Fu) > 0x60u);
-                const float f = kv_pow2(-e);
-                uint32_t hi[2], lo[2];
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const float x = kv_scaled(w[v] & 0xFFFFu, f), y = kv_scaled(w[v] >> 16, f);
-                    const uint32_t a = kv_e4m3x2(x, y), h = kv_f16x2(a);
-                    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                    const uint32_t b = kv_e4m3x2(x - back.x, y - back.y);
-                    hi[v >> 1] = (v & 1) ? (hi[v >> 1] | (a << 16)) : a;
-                    lo[v >> 1] = (v & 1) ? (lo[v >> 1] | (b << 16)) : b;
-                }
-                uint8_t* const row = q_sm + n * 128;
-                const int c2 = (D == 128) ? c : c + 8, slab2 = (D == 128) ? NT * 128 : 0;
-                *reinterpret_cast<uint2*>(row + (((c >> 1) ^ (n & 7)) << 4) + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(row + slab2 + (((c2 >> 1) ^ (n & 7)) << 4) + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
-                if (c == 0) rowf[n] = p.scale * kv_pow2(e);
-            }
-        }
+        // the shuffles above are the point where all lanes of the row hold its elements
+        uint8_t* const row = q_sm + n * 128;
+        *reinterpret_cast<uint2*>(row + (((c >> 1) ^ (n & 7)) << 4) + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(row + slab2 + (((c2 >> 1) ^ (n & 7)) << 4) + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
+        if (c == 0) rowf[n] = top < 0x7F80u ? p.scale * kv_pow2(e) : __int_as_float(0x7FC00000);
     }
     fence_proxy_async_smem();
 }
@@ -497,14 +515,16 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     uint64_t* const qfree = qready + 2;          // [2] its last S^T is complete
     uint64_t* const ofull = qfree + 2;           // [1] a segment's O^T is complete
     uint64_t* const oempty = ofull + 1;          // [1] read by the softmax warps
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(oempty + 1);
+    uint64_t* const segfull = oempty + 1;        // [SEG_RING] a segment is published
+    uint64_t* const segempty = segfull + C::SEG_RING;   // [SEG_RING] the softmax warps, the last to follow, are done with it
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(segempty + C::SEG_RING);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    float2* const page_scale = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + 512);   // [SCALE_RING][8] (K, V)
-    float* const rowf = reinterpret_cast<float*>(page_scale + C::SCALE_RING * 8);            // [ROWF_RING][NT]: score = S * rowf * K scale
+    float2* const page_scale = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + 768);   // [SCALE_RING][8] (K, V)
+    KvSeg* const segs = reinterpret_cast<KvSeg*>(page_scale + C::SCALE_RING * 8);            // [SEG_RING]
+    float* const rowf = reinterpret_cast<float*>(segs + C::SEG_RING);            // [ROWF_RING][NT]: score = S * rowf * K scale
     float* const negm = rowf + C::ROWF_RING * NT;                                            // [NT] -m
     float* const resc = negm + NT;                                                           // [NT]
-    float* const lsum = resc + NT;                                                           // [NT]
-    float* const red = lsum + NT;                                                            // [2][4][NH]
+    float* const red = resc + NT;                                                            // [2][4][NH]
     unsigned* const pre = reinterpret_cast<unsigned*>(red + 8 * NH);                         // [B + 1]
     int* const len_of = reinterpret_cast<int*>(pre + KV_MAX_BATCH + 4);                      // [B]
     uint8_t* const rows8 = reinterpret_cast<uint8_t*>(len_of + KV_MAX_BATCH);                // [B]
@@ -520,6 +540,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
         }
         for (int i = 0; i < 2; ++i) { mbar_init(&qready[i], 2); mbar_init(&qfree[i], 1); }
         mbar_init(ofull, 1); mbar_init(oempty, 8);
+        for (int i = 0; i < C::SEG_RING; ++i) { mbar_init(&segfull[i], 1); mbar_init(&segempty[i], 8); }
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -527,6 +548,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
         tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();
     }
+#pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += C::THREADS) {
         const KvRequest rq(p, b);
         const KvShape sh(rq.rows * p.group, kv_tiles(rq.len), NT);
@@ -537,27 +559,15 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) {
-        // inclusive scan of the weights
-        unsigned carry = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            unsigned v = (b0 + lane < p.B) ? pre[b0 + lane + 1] : 0u;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-                if (lane >= d) v += o;
-            }
-            v += carry;
-            if (b0 + lane < p.B) pre[b0 + lane + 1] = v;
-            carry = __shfl_sync(0xFFFFFFFFu, v, 31);
-        }
-        if (lane == 0) pre[0] = 0;
-    }
-    __syncthreads();
     const uint32_t tmem = *tmem_slot;
     const int g = blockIdx.x;
-    const KvShares shares(pre[p.B], p.ctas);
-    KvWalk walk(p, pre, len_of, rows8, shares.start(g), shares.start(g + 1), NT);
+    // segment number `i` of the CTA, once it is published; false: there is none (or the CTA has aborted)
+    auto segment = [&](uint32_t i, KvSeg& sg) -> bool {
+        const uint32_t at = i % C::SEG_RING;
+        if (!__all_sync(0xFFFFFFFFu, kv_wait(&segfull[at], (i / C::SEG_RING) & 1u, abort_flag))) return false;
+        sg = segs[at];
+        return sg.k1 > 0;
+    };
     KvSeg sg;
 
     if (warp < 4) {
@@ -570,7 +580,43 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             const uint32_t stage0 = smem_u32(stages);
             int s = 0;
             uint32_t ph = 0, issued = 0, last_ph = 0, tile = 0;
-            bool more = walk.next(sg);
+            // inclusive scan of the weights
+            unsigned carry = 0;
+#pragma unroll 1
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                unsigned v = (b0 + lane < p.B) ? pre[b0 + lane + 1] : 0u;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const unsigned o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+                    if (lane >= d) v += o;
+                }
+                v += carry;
+                if (b0 + lane < p.B) pre[b0 + lane + 1] = v;
+                carry = __shfl_sync(0xFFFFFFFFu, v, 31);
+            }
+            if (lane == 0) pre[0] = 0;
+            __syncwarp();
+            const KvShares shares(carry, p.ctas);
+            KvWalk walk(p, pre, len_of, rows8, shares.start(g), shares.start(g + 1), NT);
+            uint32_t seg = 0;
+            // the next segment, published for the others; k1 of 0 marks the end
+            auto publish = [&]() -> bool {
+                const bool there = walk.next(sg);
+                const uint32_t at = seg % C::SEG_RING;
+                if (!__all_sync(0xFFFFFFFFu, kv_wait(&segempty[at], ((seg / C::SEG_RING) & 1u) ^ 1u, abort_flag))) {
+                    if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_PRODUCER);
+                    return false;
+                }
+                if (lane == 0) {
+                    if (!there) sg.k1 = 0;
+                    segs[at] = sg;
+                    mbar_arrive(&segfull[at]);
+                }
+                __syncwarp();
+                ++seg;
+                return there;
+            };
+            bool more = publish();
             int k = more ? sg.k0 : 0;
             // the page that this lane brings in of tile k: looked up a tile ahead
             auto look = [&](int& n) -> int {
@@ -578,11 +624,12 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 return lane < n ? __ldg(p.table + (size_t)sg.b * p.width + (size_t)k * per_tile + lane) : 0;
             };
             int n = 0, id = more ? look(n) : 0;
+#pragma unroll 1
             while (more) {
                 const int cur_n = n, head = sg.head;
                 int page = id;
                 if (++k == sg.k1) {
-                    more = walk.next(sg);
+                    more = publish();
                     k = sg.k0;
                 }
                 if (more) id = look(n);
@@ -610,9 +657,10 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 if (++s == C::STAGES) { s = 0; ph ^= 1u; }
             }
             // every issued copy must land before the CTA can leave
+#pragma unroll 1
             for (int i = 0; i < C::STAGES; ++i)
                 if ((issued >> i) & 1u)
-                    if (!mbar_wait(&kvfull[i], (last_ph >> i) & 1u, TL_WAIT_LIMIT >> 4))
+                    if (!kv_drain(&kvfull[i], (last_ph >> i) & 1u))
                         if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DRAIN);
         } else if (warp < 3) {
             // ------------------------------------------------------------ MMA issuers
@@ -631,8 +679,10 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             uint32_t seg = 0;
             uint64_t* last_bar = nullptr;
             uint32_t last_par = 0;
-            while (ok && walk.next(sg)) {
+#pragma unroll 1
+            while (ok && segment(seg, sg)) {
                 const uint32_t n_bits = (uint32_t)(sg.nt >> 3) << 17;
+#pragma unroll 1
                 for (int k = sg.k0; k < sg.k1; ++k) {
                     const uint32_t b = ring.i;
                     if (warp == 1) {
@@ -676,18 +726,19 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 ++seg;
             }
             // no MMA may still run when tensor memory is released: the barrier of this warp's last ones
-            if (last_bar && !__all_sync(0xFFFFFFFFu, mbar_wait(last_bar, last_par, TL_WAIT_LIMIT >> 4)) && lane == 0)
+            if (last_bar && !__all_sync(0xFFFFFFFFu, kv_drain(last_bar, last_par)) && lane == 0)
                 tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_DRAIN);
         } else {
             // ------------------------------------------------------------ rows
             uint32_t seg = 0;
-            while (walk.next(sg)) {
+#pragma unroll 1
+            while (segment(seg, sg)) {
                 if (seg > 0) {
                     if (!__all_sync(0xFFFFFFFFu, kv_wait(&qfree[seg & 1u], ((seg >> 1) & 1u) ^ 1u, abort_flag))) {
                         if (lane == 0) tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_PRODUCER);
                         break;
                     }
-                    kv_load_rows<D, NT, 5>(p, sg, lane, 32, q_sm + (seg & 1u) * C::Q_BYTES, rowf + (seg % C::ROWF_RING) * NT);
+                    kv_load_rows<D, NT>(p, sg, lane, 32, q_sm + (seg & 1u) * C::Q_BYTES, rowf + (seg % C::ROWF_RING) * NT);
                     __syncwarp();
                     if (lane < 2) mbar_arrive(&qready[seg & 1u]);
                 }
@@ -704,6 +755,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
         const uint32_t k_off = (uint32_t)(r >> pl) * page_bytes + (uint32_t)(r & ((1 << pl) - 1)) * 16u;
         KvRing<C::STAGES> stage;
         KvRing<BUFS> ring;
+        uint32_t seg = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             if (!__all_sync(0xFFFFFFFFu, kv_wait(bar, parity, abort_flag))) {
@@ -711,7 +763,9 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 ok = false;
             }
         };
-        while (ok && walk.next(sg)) {
+#pragma unroll 1
+        while (ok && segment(seg++, sg)) {
+#pragma unroll 1
             for (int k = sg.k0; k < sg.k1; ++k, stage.step(), ring.step()) {
                 const uint32_t b = ring.i;
                 wait(&kvfull[stage.i], stage.par);
@@ -731,24 +785,22 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&kready[b]);
                 // tokens behind the request's last one count nothing, whatever their bytes are
-                const int valid = (k + 1 == sg.tiles) ? walk.last(sg.b) : KV_TILE;
-#pragma unroll
+                const int valid = (k + 1 == sg.k1) ? sg.valid : KV_TILE;
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     if (D == 128 || qd < 2) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const int t = 64 * half + 16 * c;
-                            kv_decode16(*reinterpret_cast<const uint4*>(st + (uint32_t)(t >> pl) * page_bytes + (uint32_t)(D << pl) +
-                                                                        (uint32_t)((t & ((1 << pl) - 1)) >> 4) * (16u * D) + 16u * r),
-                                        out + 8 * c);
-                        }
-                        if (valid < KV_TILE) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const int t = 64 * half + 2 * j;
-                                if (t >= valid) out[j] = 0u;
-                                else if (t + 1 >= valid) out[j] &= 0xFFFFu;
+                            const int tt = 64 * half + 16 * c;
+                            uint4 w = *reinterpret_cast<const uint4*>(st + (uint32_t)(tt >> pl) * page_bytes + (uint32_t)(D << pl) +
+                                                                      (uint32_t)((tt & ((1 << pl) - 1)) >> 4) * (16u * D) + 16u * r);
+                            if (valid < KV_TILE) {
+                                w.x = kv_first_bytes(w.x, valid - tt);
+                                w.y = kv_first_bytes(w.y, valid - tt - 4);
+                                w.z = kv_first_bytes(w.z, valid - tt - 8);
+                                w.w = kv_first_bytes(w.w, valid - tt - 12);
                             }
+                            kv_decode16(w, out + 8 * c);
                         }
                     }
                     if (half == 0) {
@@ -781,7 +833,6 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
         const uint32_t p_line = smem_u32(p_sm) + (uint32_t)((t >> 3) * C::P_STEP + (t & 7) * 32) + (((uint32_t)grp ^ ((t >> 2) & 1u)) << 4);
         float* const g_negm = negm + grp * NH;        // this group's rows, block by block
         float* const g_resc = resc + grp * NH;
-        float* const g_was = lsum + grp * NH;
         float* const g_red = red + grp * 4 * NH;
         uint32_t n = 0, seg = 0;
         KvRing<BUFS> ring;
@@ -790,9 +841,11 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             if (!__all_sync(0xFFFFFFFFu, kv_wait(bar, parity, abort_flag)) && lane == 0)
                 tc_fail(p.err, abort_flag, TL_DEV_ERR_TIMEOUT_EPILOGUE);
         };
-        while (walk.next(sg)) {
+        // whether there is a segment is for the group to agree on, after an abort too: its barriers need all of its warps
+#pragma unroll 1
+        while (!kv_group_any(bar_id, !segment(seg, sg))) {
             if (seg == 0) {
-                kv_load_rows<D, NT, 3>(p, sg, (int)threadIdx.x - 256, 256, q_sm, rowf);
+                kv_load_rows<D, NT>(p, sg, (int)threadIdx.x - 256, 256, q_sm, rowf);
                 kv_group_sync(bar_id);
                 if (t == 0) mbar_arrive(&qready[0]);
             }
@@ -801,90 +854,97 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
 #pragma unroll
             for (int i = 0; i < NH; ++i) l[i] = 0.0f;
             uint32_t was_b = 0, was_par = 0;       // the tile before: its buffer
+#pragma unroll 1
             for (int k = sg.k0; k < sg.k1; ++k) {
                 const uint32_t b = ring.i;
                 const bool first = k == sg.k0;
                 wait(&qkdone[b], ring.par);
                 tc_fence_after();
-                float x[NH];
-#pragma unroll
-                for (int j = 0; j < C::NB; ++j)
-                    if (j < nb) tmem_ld8(t_lane + (uint32_t)(C::S_COL + 16 * j + c0) + b * NT, x + 8 * j);
+                const uint32_t s_at = t_lane + (uint32_t)(C::S_COL + c0) + b * NT;
+                const float* const rf_at = rowf + (seg % C::ROWF_RING) * NT + c0;
                 const float2 sc = page_scale[8 * (n % C::SCALE_RING) + (t >> p.page_log2)];
-                const int valid = (k + 1 == sg.tiles) ? walk.last(sg.b) : KV_TILE;
+                const int valid = (k + 1 == sg.k1) ? sg.valid : KV_TILE;
                 const bool live = t < valid;
                 const float vs = live ? sc.y : 1.0f;
                 const float lv = kv_lg2(vs);
                 const uint64_t ks2 = f2_pack(sc.x, sc.x);
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sempty[b]);
-                // x = score - m
-                float top = -INFINITY;
+                float x[NH];
+                // Twice where the reference moves (in a segment's first tile it always does, and x is not needed before). The
+                // state is kept opaque, so that the code of x is there once: instruction fetches are a bound.
+                uint32_t move = first ? 1u : 0u, moved = 0;
+#pragma unroll 1
+                for (;;) {
+                    asm volatile("" : "+r"(move), "+r"(moved));
+                    if (!move) {
 #pragma unroll
-                for (int j = 0; j < C::NB; ++j) {
-                    if (j < nb) {
+                        for (int j = 0; j < C::NB; ++j)
+                            if (j < nb) tmem_ld8(s_at + 16 * j, x + 8 * j);
+                        tmem_wait_ld();
+                        // x = score - m
+                        float top = -INFINITY;
 #pragma unroll
-                        for (int i = 8 * j; i < 8 * j + 8; i += 4) {
-                            const float4 rf = *reinterpret_cast<const float4*>(rowf + (seg % C::ROWF_RING) * NT + 8 * j + c0 + i);
-                            const float4 nm = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *reinterpret_cast<const float4*>(g_negm + i);
-                            f2_unpack(f2_fma(f2_mul(f2_pack(x[i], x[i + 1]), ks2), f2_pack(rf.x, rf.y), f2_pack(nm.x, nm.y)), x[i], x[i + 1]);
-                            f2_unpack(f2_fma(f2_mul(f2_pack(x[i + 2], x[i + 3]), ks2), f2_pack(rf.z, rf.w), f2_pack(nm.z, nm.w)), x[i + 2], x[i + 3]);
+                        for (int j = 0; j < C::NB; ++j) {
+                            if (j < nb) {
+#pragma unroll
+                                for (int i = 8 * j; i < 8 * j + 8; i += 4) {
+                                    const float4 rf = *reinterpret_cast<const float4*>(rf_at + 8 * j + i);
+                                    const float4 nm = *reinterpret_cast<const float4*>(g_negm + i);
+                                    f2_unpack(f2_fma(f2_mul(f2_pack(x[i], x[i + 1]), ks2), f2_pack(rf.x, rf.y), f2_pack(nm.x, nm.y)), x[i], x[i + 1]);
+                                    f2_unpack(f2_fma(f2_mul(f2_pack(x[i + 2], x[i + 3]), ks2), f2_pack(rf.z, rf.w), f2_pack(nm.z, nm.w)), x[i + 2],
+                                              x[i + 3]);
+                                }
+#pragma unroll
+                                for (int i = 8 * j; i < 8 * j + 8; ++i) top = fmaxf(top, x[i]);
+                            }
                         }
-                        if (valid < KV_TILE) {
-#pragma unroll
-                            for (int i = 8 * j; i < 8 * j + 8; ++i) x[i] = live ? x[i] : -INFINITY;
-                        }
-#pragma unroll
-                        for (int i = 8 * j; i < 8 * j + 8; ++i) top = fmaxf(top, x[i]);
+                        if (moved || !kv_group_any(bar_id, live && top + lv > KV_SLACK)) break;
                     }
-                }
-                if (kv_group_any(bar_id, first || top + lv > KV_SLACK)) {
-                    // the reference moves: maxima of the log-weights over the tile's tokens
+                    move = 0;
+                    moved = 1;
+                    // the reference moves: maxima of the log-weights over the tile's tokens, block by block
+#pragma unroll 1
+                    for (int j = 0; j < nb; ++j) {
+                        float v[8];
+                        tmem_ld8(s_at + 16 * j, v);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < C::NB; ++j) {
-                        if (j < nb) {
-                            float v[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) v[i] = live ? (x[8 * j + i] - (first ? 0.0f : g_negm[8 * j + i])) + lv : -INFINITY;
-                            const float w = kv_across8(v, lane, [](float a_, float b_) { return fmaxf(a_, b_); });
-                            if (lane < 8) g_red[qd * NH + 8 * j + ((lane & 1) << 2) + (lane & 2) + (lane >> 2)] = w;
-                        }
+                        for (int i = 0; i < 8; ++i) v[i] = live ? fmaf(v[i] * sc.x, rf_at[16 * j + i], lv) : -INFINITY;
+                        const float w = kv_across8(v, lane, [](float a_, float b_) { return fmaxf(a_, b_); });
+                        if (lane < 8) g_red[qd * NH + 8 * j + ((lane & 1) << 2) + (lane & 2) + (lane >> 2)] = w;
                     }
                     kv_group_sync(bar_id);
                     if (t < 8 * nb) {
                         const float* const rd = g_red + t;
                         const float old = first ? -INFINITY : -g_negm[t];
                         const float now = fmaxf(old, fmaxf(fmaxf(rd[0], rd[NH]), fmaxf(rd[2 * NH], rd[3 * NH])));
-                        // what x is off by, and what O and l shrink by (nothing is held yet under an old m of minus infinity)
+                        // what O and l shrink by (nothing is held yet under an old m of minus infinity)
                         g_resc[t] = (old == -INFINITY) ? 0.0f : kv_ex2(old - now);
-                        g_was[t] = first ? 0.0f : g_negm[t];
                         g_negm[t] = -now;
                     }
                     kv_group_sync(bar_id);
-                    if (!first) wait(&pvdone[was_b], was_par);    // O holds every tile before this one
-                    tc_fence_after();
-#pragma unroll
-                    for (int j = 0; j < C::NB; ++j) {
-                        if (j < nb) {
+                    if (!first) {
+                        wait(&pvdone[was_b], was_par);                // O holds every tile before this one
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int j = 0; j < nb; ++j) {
                             float o[8];
-                            if (!first) {
-                                tmem_ld8(t_lane + (uint32_t)(C::O_COL + 16 * j + c0), o);
-                                tmem_wait_ld();
-                            }
+                            tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0) + 16 * j, o);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float f = g_resc[8 * j + i];
-                                x[8 * j + i] = (x[8 * j + i] - g_was[8 * j + i]) + g_negm[8 * j + i];
-                                if (valid < KV_TILE) x[8 * j + i] = live ? x[8 * j + i] : -INFINITY;
-                                l[8 * j + i] *= f;
-                                o[i] *= f;
-                            }
-                            if (!first) tmem_st8(t_lane + (uint32_t)(C::O_COL + 16 * j + c0), o);
+                            for (int i = 0; i < 8; ++i) o[i] *= g_resc[8 * j + i];
+                            tmem_st8(t_lane + (uint32_t)(C::O_COL + c0) + 16 * j, o);
                         }
+                        tmem_wait_st();
+#pragma unroll
+                        for (int i = 0; i < NH; ++i) l[i] *= g_resc[i];        // rows without work hold nothing that counts
                     }
-                    if (!first) tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sempty[b]);
+                if (!live) {
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) x[i] = -INFINITY;
                 }
                 wait(&pvdone[b], ring.par ^ 1u);                  // the O^T that read this P buffer last
                 const float vs8 = vs * 256.0f;                    // 2^KV_P_SHIFT
@@ -937,22 +997,21 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             }
             wait(ofull, seg & 1u);
             tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < nb; ++j) {
+                float o[8];
+                tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0) + 16 * j, o);
+                tmem_wait_ld();
+                if (D == 128 || qd < 2) {
+                    float* const to = p.part_o + (slot + 16 * j + c0) * D + t;
 #pragma unroll
-            for (int j = 0; j < C::NB; ++j) {
-                if (j < nb) {
-                    float o[8];
-                    tmem_ld8(t_lane + (uint32_t)(C::O_COL + 16 * j + c0), o);
-                    tmem_wait_ld();
-                    if (D == 128 || qd < 2) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (16 * j + c0 + i < sg.n_rows) p.part_o[(slot + 16 * j + c0 + i) * D + t] = o[i];
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        if (16 * j + c0 + i < sg.n_rows) to[i * D] = o[i];
                 }
             }
             tc_fence_before();
             kv_group_sync(bar_id);            // red and negm may change again
-            if (lane == 0) mbar_arrive(oempty);
+            if (lane == 0) { mbar_arrive(oempty); mbar_arrive(&segempty[seg % C::SEG_RING]); }
             ++seg;
         }
     }
@@ -998,6 +1057,7 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
     }
     // this request's place in the tile list
     unsigned before = 0, all = 0;
+#pragma unroll 1
     for (int i = tid; i < p.B; i += KV_MERGE_THREADS) {
         const KvRequest other(p, i);
         const KvShape sh(other.rows * p.group, kv_tiles(other.len), p.nt);
@@ -1031,7 +1091,7 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
         const uint4* const qr = reinterpret_cast<const uint4*>(p.q + (size_t)row * p.q_stride + (size_t)h * D);
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (sees) {
-#pragma unroll
+#pragma unroll 4
             for (int c = 0; c < D / 8; ++c) {
                 const uint4 a = *reinterpret_cast<const uint4*>(kn + lane * RP + 8 * c), w = __ldg(qr + c);
                 const uint32_t ka[4] = {a.x, a.y, a.z, a.w}, qa[4] = {w.x, w.y, w.z, w.w};
