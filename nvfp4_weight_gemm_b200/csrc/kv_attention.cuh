@@ -215,8 +215,8 @@ struct KvWalk {
 //   * warp 3        the rows: Q of the next segment to one of two buffers in shared memory. The first segment's Q is
 //                   brought in by the softmax warps, which have nothing to do yet.
 //   * warps 4..7    movers: K (lane = token), then V, converted (lane = channel), 16 bytes of a lane at a time.
-//   * warps 8..15   softmax: two groups of four warps, every other block of 8 rows each, lane = token; blocks without rows
-//                   are passed over. A group also reads its rows of O (lane = channel) when a segment ends and writes
+//   * warps 8..15   softmax: two groups of four warps, half of the blocks of 8 rows each, lane = token; blocks without
+//                   rows are passed over. A group also reads its rows of O (lane = channel) when a segment ends and writes
 //                   the part.
 // Every mbarrier wait is bounded; after one has run out the others return at once, every role runs to its end
 // (so no named barrier is left waiting), and the status word is set.
@@ -231,7 +231,7 @@ struct KvCfg {
     static constexpr int REGS_CONTROL = 96, REGS_MOVE = 96, REGS_SOFTMAX = 160;
     static_assert(REGS_CONTROL + REGS_MOVE + 2 * REGS_SOFTMAX <= 512, "registers of the launch");
     static constexpr int NH = NT / 2;                          // rows of a softmax group
-    static constexpr int NB = NT / 16;                         // blocks of 8 of a softmax group
+    static constexpr int NB = NT / 16;                         // blocks of 8 rows of a softmax group at most
     static constexpr int STAGE_BYTES = 2 * KV_TILE * D;
     static constexpr int QSTEPS = 2 * D / 32;                  // MMAs of S^T: 32 channels each, both terms
     static constexpr int Q_BYTES = NT * D * 2;                 // slabs of [NT] 128-byte rows, swizzled: the first terms, the second
@@ -276,6 +276,13 @@ struct KvCfg {
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+                   "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
                  : "r"(taddr));
 }
 
@@ -827,10 +834,10 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
         // ------------------------------------------------------------ softmax
         regs_inc<C::REGS_SOFTMAX>();
         const int grp = (warp - 8) >> 2, qd = warp & 3, t = 32 * qd + lane;     // token of the tile; channel
-        const int c0 = 8 * grp, bar_id = 1 + grp;                                // block j of 8 rows begins at row 16 j + c0
+        const int bar_id = 1 + grp;
         const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16);
         // this token's rows in P: 16-byte units of 8 rows, two a 32-byte line, swapped in every other four tokens
-        const uint32_t p_line = smem_u32(p_sm) + (uint32_t)((t >> 3) * C::P_STEP + (t & 7) * 32) + (((uint32_t)grp ^ ((t >> 2) & 1u)) << 4);
+        const uint32_t p_line = smem_u32(p_sm) + (uint32_t)((t >> 3) * C::P_STEP + (t & 7) * 32);
         float* const g_negm = negm + grp * NH;        // this group's rows, block by block
         float* const g_resc = resc + grp * NH;
         float* const g_red = red + grp * 4 * NH;
@@ -849,7 +856,14 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 kv_group_sync(bar_id);
                 if (t == 0) mbar_arrive(&qready[0]);
             }
-            const int nb = (sg.n_rows - c0 + 15) >> 4;               // blocks of this group that hold rows
+            // this group's blocks of 8 rows: nb of them from row c0 (the first group has one more if they are odd)
+            const int blocks = (sg.n_rows + 7) >> 3;
+            const int nb = grp ? blocks >> 1 : (blocks + 1) >> 1, c0 = grp ? 8 * ((blocks + 1) >> 1) : 0;
+            // where a block lies in this token's lines of P
+            auto p_unit = [&](int j) -> uint32_t {
+                const uint32_t u = (uint32_t)(c0 >> 3) + j;
+                return (u >> 1) * C::P_ATOM + (((u ^ (t >> 2)) & 1u) << 4);
+            };
             float l[NH];
 #pragma unroll
             for (int i = 0; i < NH; ++i) l[i] = 0.0f;
@@ -876,27 +890,38 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 for (;;) {
                     asm volatile("" : "+r"(move), "+r"(moved));
                     if (!move) {
+                        // x = score - m; a full group's blocks in one piece (without branches between them the loads and the
+                        // chains of different blocks overlap), others one by one
+                        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        auto scores = [&](int j) {
 #pragma unroll
-                        for (int j = 0; j < C::NB; ++j)
-                            if (j < nb) tmem_ld8(s_at + 16 * j, x + 8 * j);
-                        tmem_wait_ld();
-                        // x = score - m
-                        float top = -INFINITY;
-#pragma unroll
-                        for (int j = 0; j < C::NB; ++j) {
-                            if (j < nb) {
-#pragma unroll
-                                for (int i = 8 * j; i < 8 * j + 8; i += 4) {
-                                    const float4 rf = *reinterpret_cast<const float4*>(rf_at + 8 * j + i);
-                                    const float4 nm = *reinterpret_cast<const float4*>(g_negm + i);
-                                    f2_unpack(f2_fma(f2_mul(f2_pack(x[i], x[i + 1]), ks2), f2_pack(rf.x, rf.y), f2_pack(nm.x, nm.y)), x[i], x[i + 1]);
-                                    f2_unpack(f2_fma(f2_mul(f2_pack(x[i + 2], x[i + 3]), ks2), f2_pack(rf.z, rf.w), f2_pack(nm.z, nm.w)), x[i + 2],
-                                              x[i + 3]);
-                                }
-#pragma unroll
-                                for (int i = 8 * j; i < 8 * j + 8; ++i) top = fmaxf(top, x[i]);
+                            for (int i = 8 * j; i < 8 * j + 8; i += 4) {
+                                const float4 rf = *reinterpret_cast<const float4*>(rf_at + i);
+                                const float4 nm = *reinterpret_cast<const float4*>(g_negm + i);
+                                f2_unpack(f2_fma(f2_mul(f2_pack(x[i], x[i + 1]), ks2), f2_pack(rf.x, rf.y), f2_pack(nm.x, nm.y)), x[i], x[i + 1]);
+                                f2_unpack(f2_fma(f2_mul(f2_pack(x[i + 2], x[i + 3]), ks2), f2_pack(rf.z, rf.w), f2_pack(nm.z, nm.w)), x[i + 2],
+                                          x[i + 3]);
                             }
+#pragma unroll
+                            for (int i = 8 * j; i < 8 * j + 8; ++i) tops[i & 3] = fmaxf(tops[i & 3], x[i]);
+                        };
+                        if (nb == C::NB) {
+#pragma unroll
+                            for (int j = 0; j + 1 < C::NB; j += 2) tmem_ld16f(s_at + 8 * j, x + 8 * j);
+                            if (C::NB & 1) tmem_ld8(s_at + 8 * (C::NB - 1), x + 8 * (C::NB - 1));
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < C::NB; ++j) scores(j);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j + 1 < C::NB; ++j)
+                                if (j < nb) {
+                                    tmem_ld8(s_at + 8 * j, x + 8 * j);
+                                    tmem_wait_ld();
+                                    scores(j);
+                                }
                         }
+                        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                         if (moved || !kv_group_any(bar_id, live && top + lv > KV_SLACK)) break;
                     }
                     move = 0;
@@ -905,10 +930,10 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
 #pragma unroll 1
                     for (int j = 0; j < nb; ++j) {
                         float v[8];
-                        tmem_ld8(s_at + 16 * j, v);
+                        tmem_ld8(s_at + 8 * j, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = live ? fmaf(v[i] * sc.x, rf_at[16 * j + i], lv) : -INFINITY;
+                        for (int i = 0; i < 8; ++i) v[i] = live ? fmaf(v[i] * sc.x, rf_at[8 * j + i], lv) : -INFINITY;
                         const float w = kv_across8(v, lane, [](float a_, float b_) { return fmaxf(a_, b_); });
                         if (lane < 8) g_red[qd * NH + 8 * j + ((lane & 1) << 2) + (lane & 2) + (lane >> 2)] = w;
                     }
@@ -928,11 +953,11 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
 #pragma unroll 1
                         for (int j = 0; j < nb; ++j) {
                             float o[8];
-                            tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0) + 16 * j, o);
+                            tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0) + 8 * j, o);
                             tmem_wait_ld();
 #pragma unroll
                             for (int i = 0; i < 8; ++i) o[i] *= g_resc[8 * j + i];
-                            tmem_st8(t_lane + (uint32_t)(C::O_COL + c0) + 16 * j, o);
+                            tmem_st8(t_lane + (uint32_t)(C::O_COL + c0) + 8 * j, o);
                         }
                         tmem_wait_st();
 #pragma unroll
@@ -950,21 +975,26 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                 const float vs8 = vs * 256.0f;                    // 2^KV_P_SHIFT
                 const uint64_t vs2 = f2_pack(vs8, vs8);
                 const uint32_t at = p_line + b * C::P_BYTES;
+                auto weights = [&](int j) {
+                    uint32_t h[4];
 #pragma unroll
-                for (int j = 0; j < C::NB; ++j) {
-                    if (j < nb) {
-                        uint32_t h[4];
-#pragma unroll
-                        for (int i = 0; i < 8; i += 2) {
-                            const int c = 8 * j + i;
-                            const uint64_t e2 = f2_pack(kv_ex2(x[c]), kv_ex2(x[c + 1]));
-                            f2_unpack(f2_add(f2_pack(l[c], l[c + 1]), e2), l[c], l[c + 1]);
-                            float w0, w1;
-                            f2_unpack(f2_mul(e2, vs2), w0, w1);
-                            h[i >> 1] = kv_pack_f16(w0, w1);
-                        }
-                        sts_128(at + j * C::P_ATOM, h[0], h[1], h[2], h[3]);
+                    for (int i = 0; i < 8; i += 2) {
+                        const int c = 8 * j + i;
+                        const uint64_t e2 = f2_pack(kv_ex2(x[c]), kv_ex2(x[c + 1]));
+                        f2_unpack(f2_add(f2_pack(l[c], l[c + 1]), e2), l[c], l[c + 1]);
+                        float w0, w1;
+                        f2_unpack(f2_mul(e2, vs2), w0, w1);
+                        h[i >> 1] = kv_pack_f16(w0, w1);
                     }
+                    sts_128(at + p_unit(j), h[0], h[1], h[2], h[3]);
+                };
+                if (nb == C::NB) {
+#pragma unroll
+                    for (int j = 0; j < C::NB; ++j) weights(j);
+                } else {
+#pragma unroll
+                    for (int j = 0; j + 1 < C::NB; ++j)
+                        if (j < nb) weights(j);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -989,7 +1019,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             const size_t slot = (((size_t)sg.b * p.heads + sg.head) * p.row_tiles + sg.rt + g) * NT;
             kv_group_sync(bar_id);
             {
-                const int row = 16 * (t >> 3) + c0 + (t & 7);
+                const int row = c0 + t;
                 if (t < 8 * nb && row < sg.n_rows) {
                     const float* const rd = g_red + t;
                     p.part_ml[slot + row] = make_float2(-g_negm[t] - KV_P_SHIFT, 256.0f * ((rd[0] + rd[NH]) + (rd[2 * NH] + rd[3 * NH])));
@@ -1000,13 +1030,13 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
 #pragma unroll 1
             for (int j = 0; j < nb; ++j) {
                 float o[8];
-                tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0) + 16 * j, o);
+                tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0) + 8 * j, o);
                 tmem_wait_ld();
                 if (D == 128 || qd < 2) {
-                    float* const to = p.part_o + (slot + 16 * j + c0) * D + t;
+                    float* const to = p.part_o + (slot + 8 * j + c0) * D + t;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        if (16 * j + c0 + i < sg.n_rows) to[i * D] = o[i];
+                        if (8 * j + c0 + i < sg.n_rows) to[i * D] = o[i];
                 }
             }
             tc_fence_before();
