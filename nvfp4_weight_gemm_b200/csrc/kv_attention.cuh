@@ -388,13 +388,31 @@ __device__ __forceinline__ uint32_t kv_first_bytes(uint32_t w, int n) {
     return n >= 4 ? w : n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], E4M3 operands, fp32 accumulate.
-__device__ __forceinline__ void mma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem], fp32 accumulate, by the one lane whose `on` is set, of a converged warp: f16 operands, and
+// E4M3 ones. (The predicate in the instruction: 16 to 42 cycles an MMA of 16 to 80 rows back to back; in a branch of that lane
+// 25 to 42, and 127 where the compiler did not know the warp's index as uniform.)
+__device__ __forceinline__ void mma_f16_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on) : "memory");
+}
+__device__ __forceinline__ void mma_f8_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on) : "memory");
+}
+// Arrive once on `bar` when every MMA issued so far by that lane has completed.
+__device__ __forceinline__ void mma_commit_if(uint32_t on, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(smem_u32(bar)), "r"(on) : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -514,8 +532,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     uint64_t* const kvempty = kvfull + 8;        // [8] read by the movers
     uint64_t* const kready = kvempty + 8;        // [4] K tile in tensor memory
     uint64_t* const qkdone = kready + 4;         // [4] S^T complete (and the K tile free)
-    uint64_t* const sempty = qkdone + 4;         // [4] S^T read by the softmax warps
-    uint64_t* const vready = sempty + 4;         // [4] V tile in tensor memory
+    uint64_t* const vready = qkdone + 4;         // [4] V tile in tensor memory
     uint64_t* const pready = vready + 4;         // [4] P in shared memory, O rescaled if need be
     uint64_t* const pvdone = pready + 4;         // [4] O^T has the tile (and the V tile and P are free)
     uint64_t* const qready = pvdone + 4;         // [2] Q of a segment in shared memory
@@ -536,13 +553,14 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
     int* const len_of = reinterpret_cast<int*>(pre + KV_MAX_BATCH + 4);                      // [B]
     uint8_t* const rows8 = reinterpret_cast<uint8_t*>(len_of + KV_MAX_BATCH);                // [B]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the warp's index from one lane: the compiler then knows the roles' code as uniform, which an MMA's operands have to be
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     // the merge may be brought up now; it waits for this launch's parts by itself
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) { mbar_init(&kvfull[i], 33); mbar_init(&kvempty[i], 4); }
         for (int i = 0; i < BUFS; ++i) {
-            mbar_init(&kready[i], 4); mbar_init(&qkdone[i], 1); mbar_init(&sempty[i], 8);
+            mbar_init(&kready[i], 4); mbar_init(&qkdone[i], 1);
             mbar_init(&vready[i], 4); mbar_init(&pready[i], 8); mbar_init(&pvdone[i], 1);
         }
         for (int i = 0; i < 2; ++i) { mbar_init(&qready[i], 2); mbar_init(&qfree[i], 1); }
@@ -674,7 +692,7 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             const uint32_t tmem_u = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             const uint64_t qdesc = kv_uniform64(smem_desc_k_sw128(smem_u32(q_sm)));
             const uint64_t pdesc = kv_uniform64(smem_desc_mn_sw32(smem_u32(p_sm), C::P_ATOM, C::P_STEP));
-            const bool leader = elect_one();
+            const uint32_t leader = elect_one() ? 1u : 0u;
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 if (ok && !__all_sync(0xFFFFFFFFu, kv_wait(bar, parity, abort_flag))) {
@@ -695,18 +713,18 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                     if (warp == 1) {
                         if (k == sg.k0) wait(&qready[seg & 1u], (seg >> 1) & 1u);
                         wait(&kready[b], ring.par);
-                        wait(&sempty[b], ring.par ^ 1u);
+                        wait(&pvdone[b], ring.par ^ 1u);          // S^T's buffer and P's: O^T has the tile that lay there last
                         if (!ok) break;
                         tc_fence_after();
-                        if (leader) {
+                        {
                             const uint64_t qd = qdesc + (uint64_t)((seg & 1u) * (C::Q_BYTES >> 4));
                             const uint32_t d = tmem_u + (uint32_t)(C::S_COL) + b * NT, a = tmem_u + (uint32_t)C::K_COL + b * C::K_COLS;
 #pragma unroll
                             for (int i = 0; i < C::QSTEPS; ++i)
-                                mma_ts_f8(d, a + 8u * (i % (D / 32)), qd + (uint64_t)(((i >> 2) * NT * 128 + (i & 3) * 32) >> 4),
+                                mma_f8_if(leader, d, a + 8u * (i % (D / 32)), qd + (uint64_t)(((i >> 2) * NT * 128 + (i & 3) * 32) >> 4),
                                           C::IDESC_QK | n_bits, i ? 1u : 0u);
-                            mma_commit(&qkdone[b]);
-                            if (k + 1 == sg.k1) mma_commit(&qfree[seg & 1u]);
+                            mma_commit_if(leader, &qkdone[b]);
+                            if (k + 1 == sg.k1) mma_commit_if(leader, &qfree[seg & 1u]);
                         }
                         last_bar = &qkdone[b];
                     } else {
@@ -715,14 +733,14 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                         wait(&pready[b], ring.par);
                         if (!ok) break;
                         tc_fence_after();
-                        if (leader) {
+                        {
                             const uint64_t pd = pdesc + (uint64_t)(b * (C::P_BYTES >> 4));
 #pragma unroll
                             for (int i = 0; i < KV_TILE / 16; ++i)
-                                mma_ts_f16(tmem_u + (uint32_t)C::O_COL, tmem_u + (uint32_t)(C::V_COL + 8 * i) + b * C::V_COLS,
+                                mma_f16_if(leader, tmem_u + (uint32_t)C::O_COL, tmem_u + (uint32_t)(C::V_COL + 8 * i) + b * C::V_COLS,
                                            pd + (uint64_t)((2 * i * C::P_STEP) >> 4), C::IDESC_PV | n_bits, (i || k != sg.k0) ? 1u : 0u);
-                            mma_commit(&pvdone[b]);
-                            if (k + 1 == sg.k1) mma_commit(ofull);
+                            mma_commit_if(leader, &pvdone[b]);
+                            if (k + 1 == sg.k1) mma_commit_if(leader, ofull);
                         }
                         last_bar = &pvdone[b];
                     }
@@ -964,14 +982,10 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
                         for (int i = 0; i < NH; ++i) l[i] *= g_resc[i];        // rows without work hold nothing that counts
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sempty[b]);
                 if (!live) {
 #pragma unroll
                     for (int i = 0; i < NH; ++i) x[i] = -INFINITY;
                 }
-                wait(&pvdone[b], ring.par ^ 1u);                  // the O^T that read this P buffer last
                 const float vs8 = vs * 256.0f;                    // 2^KV_P_SHIFT
                 const uint64_t vs2 = f2_pack(vs8, vs8);
                 const uint32_t at = p_line + b * C::P_BYTES;
