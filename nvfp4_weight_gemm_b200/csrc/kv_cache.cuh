@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <type_traits>
 
 namespace tl {
 
@@ -46,6 +47,7 @@ struct KvSlotsParams {
 };
 
 constexpr int KV_SLOTS_THREADS = 1024;
+constexpr int KV_SLOTS_A_CTA = 2048;        // slots of a CTA before the cluster grows (up to 8 CTAs)
 
 // Inclusive scan of one value a thread over the block (1024 threads); `total` gets the sum.
 __device__ __forceinline__ unsigned long long kv_block_scan(unsigned long long v, unsigned long long* warp_sums,
@@ -88,7 +90,8 @@ __device__ __forceinline__ int kv_find(const int* pre, int B, int i) {
 // One thread a request; the pages and slots of all requests are then dealt out over the threads of
 // the launch, each finding its request in the prefix sums. Launched as one CTA, or as one cluster of
 // CTAs that repeat the scan and share the dealing out when there are many slots. Latency-bound: a
-// few dependent reads of the request arrays, the stack and the table.
+// few dependent reads of the request arrays, the stack and the table. Two calls of 64 requests with 8 slots each: 16.5 us
+// on one CTA, as on eight; of 1000 requests with 8 slots each 84 us on one and 29 on eight, with 300 each 142 and 35.
 __global__ void __launch_bounds__(KV_SLOTS_THREADS, 1) kv_slots_kernel(const KvSlotsParams p) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
@@ -167,16 +170,28 @@ __global__ void __launch_bounds__(KV_SLOTS_THREADS, 1) kv_slots_kernel(const KvS
         }
     }
     if (ranks > 1) cluster.sync(); else __syncthreads();
-    const int n_slots = pre_add[p.B];
-    for (int i = t0; i < p.max_slots; i += step) {
-        int slot = -1;
-        if (i < n_slots) {
-            const int r = kv_find(pre_add, p.B, i);
-            const int pos = len_of[r] + (i - pre_add[r]);
-            const int page = __ldcg(p.table + (size_t)r * p.width + (pos >> p.page_log2));
-            if (page >= 0) slot = (page << p.page_log2) + (pos & (P - 1));
+    // a warp takes 128 slots at a time, 32 side by side; a lane searches for the first and looks whether the request of
+    // the last one still holds the next
+    const int n_slots = pre_add[p.B], lane = b & 31;
+    for (long long i0 = (t0 >> 5) * 128; i0 < p.max_slots; i0 += 4 * step) {
+        int page[4], r = 0;
+        int pos[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const long long i = i0 + 32 * u + lane;
+            page[u] = -1;
+            pos[u] = 0;
+            if (i < n_slots) {
+                if (u == 0 || i >= pre_add[r + 1]) r = kv_find(pre_add, p.B, (int)i);
+                pos[u] = len_of[r] + ((int)i - pre_add[r]);
+                page[u] = __ldcg(p.table + (size_t)r * p.width + (pos[u] >> p.page_log2));
+            }
         }
-        p.slots[i] = slot;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const long long i = i0 + 32 * u + lane;
+            if (i < p.max_slots) p.slots[i] = page[u] >= 0 ? (page[u] << p.page_log2) + (pos[u] & (P - 1)) : -1;
+        }
     }
 }
 
@@ -227,6 +242,13 @@ __device__ __forceinline__ float kv_scaled(uint32_t bits16, float inv) {
     return ((bits16 & 0x7F80u) == 0x7F80u) ? __int_as_float(0x7FC00000) : x * inv;
 }
 
+// Two E4M3 bytes of bf16 values (in the upper halves) times `inv`. ODD: there may be infinities and NaN.
+template <bool ODD>
+__device__ __forceinline__ uint32_t kv_bytes2(uint32_t a, uint32_t b, float inv) {
+    if (ODD) return kv_e4m3x2(kv_scaled(a >> 16, inv), kv_scaled(b >> 16, inv));
+    return kv_e4m3x2(__int_as_float((int)a) * inv, __int_as_float((int)b) * inv);
+}
+
 // Four bytes of a page moved to a scale 2^shift times smaller in value (shift <= 0): every value is
 // multiplied by 2^shift and rounded to E4M3 again (exact unless it becomes subnormal).
 __device__ __forceinline__ uint32_t kv_moved(uint32_t w, float factor) {
@@ -245,11 +267,15 @@ __device__ __forceinline__ uint32_t kv_moved(uint32_t w, float factor) {
 // rows of its head into shared memory, finds their largest finite magnitude, and with it the page's
 // scale, moves the bytes that the page holds already if the scale grew, and writes the new ones.
 // A page whose first token is written takes no notice of what it held. Bytes behind the run stay.
-// Bound: the bytes of the rows (bf16 in, E4M3 out) for prompts, latency for a few tokens.
+// A page whose scale grows is read and written once more. For prompts the rows' bytes are the bound (bf16 in, E4M3 out:
+// 2 x 16k tokens of 8 heads take 42 us, 31 at copy speed), so the instructions an element are few: maxima and the test for
+// infinities on packed halves, two channels of V a thread; 64 registers keep eight CTAs on an SM. For a few tokens it is
+// latency, two dependent reads (slots, rows) and the page's: 4 us.
 template <int D>
-__global__ void __launch_bounds__(KV_COMMIT_THREADS) kv_commit_kernel(const KvCommitParams p) {
+__global__ void __launch_bounds__(KV_COMMIT_THREADS, 8) kv_commit_kernel(const KvCommitParams p) {
     constexpr int RP = D + 8;                     // padded row in elements: 16-byte column reads of 8 lanes spread over the banks
     extern __shared__ __nv_bfloat16 rows[];       // [P][RP]
+    __shared__ int sl[2 * KV_COMMIT_THREADS];     // slots of tokens i0 - 1 .. i0 + chunk + P - 2, all that a run may reach
     __shared__ unsigned begins[4];                // bit i of word i / 32: a run begins at token i of the chunk
     __shared__ unsigned tops[4];
     const int P = 1 << p.page_log2;
@@ -259,13 +285,18 @@ __global__ void __launch_bounds__(KV_COMMIT_THREADS) kv_commit_kernel(const KvCo
     const long long places = (long long)p.n_pages << p.page_log2;
     const __nv_bfloat16* const x = (side ? p.v : p.k) + (size_t)head * D;
 
+#pragma unroll
+    for (int j = tid; j < 2 * KV_COMMIT_THREADS; j += KV_COMMIT_THREADS) {
+        const int i = i0 - 1 + j;
+        sl[j] = (j < p.chunk + P && i >= 0 && i < p.n) ? __ldg(p.slots + i) : -2;      // -2: follows nothing
+    }
+    __syncthreads();
     {
         bool begin = false;
-        const int i = i0 + tid;
-        if (tid < p.chunk && i < p.n) {
-            const int s = p.slots[i];
+        if (tid < p.chunk) {
+            const int s = sl[tid + 1];
             if (s >= places) atomicCAS(p.err, 0, TL_DEV_ERR_KV_SLOT);
-            begin = s >= 0 && s < places && ((s & (P - 1)) == 0 || i == 0 || p.slots[i - 1] != s - 1);
+            begin = s >= 0 && s < places && ((s & (P - 1)) == 0 || sl[tid] != s - 1);
         }
         const unsigned m = __ballot_sync(0xFFFFFFFFu, begin);
         if (lane == 0) begins[warp] = m;
@@ -274,13 +305,13 @@ __global__ void __launch_bounds__(KV_COMMIT_THREADS) kv_commit_kernel(const KvCo
     for (int w = 0; w < KV_COMMIT_THREADS / 32; ++w) {
         for (unsigned todo = begins[w]; todo; todo &= todo - 1) {
             const int first = i0 + 32 * w + __ffs(todo) - 1;
-            const int slot = p.slots[first];
+            const int slot = sl[first - i0 + 1];
             const int page = slot >> p.page_log2, off = slot & (P - 1);
             // the run's length
             int m = 1;
             {
                 const int most = min(P - off, p.n - first);
-                bool goes = tid >= 1 && tid < most && p.slots[first + tid] == slot + tid;
+                bool goes = tid >= 1 && tid < most && sl[first - i0 + 1 + tid] == slot + tid;
                 const unsigned g = __ballot_sync(0xFFFFFFFFu, goes || tid == 0);
                 __shared__ unsigned follows[4];
                 if (lane == 0) follows[warp] = g;
@@ -297,23 +328,42 @@ __global__ void __launch_bounds__(KV_COMMIT_THREADS) kv_commit_kernel(const KvCo
             uint8_t* const at = p.pages + (((size_t)page * p.heads + head) * 2 + side) * ((size_t)P * D);
             float* const scale = p.scales + ((size_t)page * p.heads + head) * 2 + side;
             const float was = off ? *scale : 0.0f;
-            // rows into shared memory, and the largest finite magnitude (bf16 magnitudes order as integers)
-            unsigned top = 0;
-            for (int e = tid; e < m * (D / 8); e += KV_COMMIT_THREADS) {
-                const int t = e / (D / 8), c = e % (D / 8);
-                int row = p.src ? p.src[first + t] : first + t;
-                uint4 q = make_uint4(0, 0, 0, 0);
-                if (row >= 0 && row < p.n_rows)
-                    q = *reinterpret_cast<const uint4*>(x + (size_t)row * p.stride + 8 * c);
-                else
-                    atomicCAS(p.err, 0, TL_DEV_ERR_KV_SLOT);
-                *reinterpret_cast<uint4*>(rows + t * RP + 8 * c) = q;
-                const uint32_t ws[4] = {q.x, q.y, q.z, q.w};
+            // rows into shared memory, eight loads of a thread in flight, and the largest finite magnitude (bf16 magnitudes
+            // order as integers)
+            unsigned top = 0, top2 = 0;             // top2: of the elements in lower and in upper halves
+            bool outside = false;                   // a row that is not there
+            constexpr int LPR = D / 8, STEP = KV_COMMIT_THREADS / LPR;      // lanes of a row, rows at a time
+            const int c = tid % LPR;
+#pragma unroll 1
+            for (int t0 = tid / LPR; t0 < m; t0 += 8 * STEP) {
+                uint4 q[8];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const unsigned lo = ws[u] & 0x7FFFu, hi = (ws[u] >> 16) & 0x7FFFu;
-                    if (lo < 0x7F80u) top = max(top, lo);
-                    if (hi < 0x7F80u) top = max(top, hi);
+                for (int j = 0; j < 8; ++j) {
+                    const int t = t0 + j * STEP;
+                    q[j] = make_uint4(0, 0, 0, 0);
+                    if (t < m) {
+                        const int row = p.src ? __ldg(p.src + first + t) : first + t;
+                        if (row >= 0 && row < p.n_rows)
+                            q[j] = __ldcs(reinterpret_cast<const uint4*>(x + (size_t)row * p.stride + 8 * c));
+                        else
+                            outside = true;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (t0 + j * STEP < m) *reinterpret_cast<uint4*>(rows + (t0 + j * STEP) * RP + 8 * c) = q[j];
+                    top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(q[j].x & 0x7FFF7FFFu, q[j].y & 0x7FFF7FFFu),
+                                                   __vmaxu2(q[j].z & 0x7FFF7FFFu, q[j].w & 0x7FFF7FFFu)));
+                }
+            }
+            if (outside) atomicCAS(p.err, 0, TL_DEV_ERR_KV_SLOT);
+            top = max(top2 & 0xFFFFu, top2 >> 16);
+            const bool odd = __syncthreads_or(top >= 0x7F80u);      // there are infinities or NaN: the largest of the others
+            if (odd) {
+                top = 0;
+                for (int e = tid; e < m * D; e += KV_COMMIT_THREADS) {
+                    const unsigned h = reinterpret_cast<const unsigned short*>(rows)[(e / D) * RP + e % D] & 0x7FFFu;
+                    if (h < 0x7F80u) top = max(top, h);
                 }
             }
             top = __reduce_max_sync(0xFFFFFFFFu, top);
@@ -327,66 +377,97 @@ __global__ void __launch_bounds__(KV_COMMIT_THREADS) kv_commit_kernel(const KvCo
                 e = max(e, e_was);
             }
             const float inv = kv_pow2(-e), factor = kv_pow2(max(e_was - e, -126));
-            const bool moves = off > 0 && e_was != e;
+            if (off > 0 && e_was != e) {
+                // the bytes in front of the run move to the page's new scale, two 16-byte groups of a thread in flight
+                const int n_old = side ? ((off + 15) >> 4) * D : off * (D / 16);
+                const unsigned inv_off = ((1u << 20) + off - 1) / off;      // u / off = u * inv_off >> 20 for u < 1024, off < 128
+#pragma unroll 1
+                for (int u0 = tid; u0 < n_old; u0 += 2 * KV_COMMIT_THREADS) {
+                    uint4* at_u[2];
+                    uint4 q[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int u = u0 + j * KV_COMMIT_THREADS, cu = (int)((unsigned)u * inv_off >> 20);
+                        at_u[j] = reinterpret_cast<uint4*>(at) + (side ? u : cu * P + (u - cu * off));
+                        if (u < n_old) q[j] = *at_u[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int u = u0 + j * KV_COMMIT_THREADS;
+                        if (u >= n_old) break;
+                        uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            // of a V group that the run begins in, the bytes from there on stay
+                            const int nb = side ? min(max(off - (u / D * 16 + 4 * i), 0), 4) : 4;
+                            const uint32_t keep = nb == 4 ? 0xFFFFFFFFu : (1u << (8 * nb)) - 1u;
+                            w[i] = (kv_moved(w[i], factor) & keep) | (w[i] & ~keep);
+                        }
+                        *at_u[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                __syncthreads();      // the run writes single bytes of such a group
+            }
             if (side == 0) {
                 // K: 16-byte groups (16 channels of a token), tokens fastest
-                if (moves)
-                    for (int u = tid; u < off * (D / 16); u += KV_COMMIT_THREADS) {
-                        uint4* const g = reinterpret_cast<uint4*>(at + ((size_t)(u / off) * P + u % off) * 16);
-                        uint4 q = *g;
-                        q.x = kv_moved(q.x, factor); q.y = kv_moved(q.y, factor);
-                        q.z = kv_moved(q.z, factor); q.w = kv_moved(q.w, factor);
-                        *g = q;
-                    }
-                for (int u = tid; u < m * (D / 16); u += KV_COMMIT_THREADS) {
-                    const int c = u / m, t = u % m;
-                    const uint4 a = *reinterpret_cast<const uint4*>(rows + t * RP + 16 * c);
-                    const uint4 b = *reinterpret_cast<const uint4*>(rows + t * RP + 16 * c + 8);
-                    const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                    uint32_t out[4];
+                const unsigned inv_m = ((1u << 20) + m - 1) / m;      // u / m = u * inv_m >> 20 for u < 1024, m <= 128
+                auto convert = [&](auto odd_) {
+                    constexpr bool ODD = decltype(odd_)::value;
+#pragma unroll 1
+                    for (int u = tid; u < m * (D / 16); u += KV_COMMIT_THREADS) {
+                        const int c = (int)((unsigned)u * inv_m >> 20), t = u - c * m;
+                        const uint4 a = *reinterpret_cast<const uint4*>(rows + t * RP + 16 * c);
+                        const uint4 b = *reinterpret_cast<const uint4*>(rows + t * RP + 16 * c + 8);
+                        const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                        uint32_t out[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        out[j] = kv_e4m3x2(kv_scaled(in[2 * j] & 0xFFFFu, inv), kv_scaled(in[2 * j] >> 16, inv)) |
-                                 (kv_e4m3x2(kv_scaled(in[2 * j + 1] & 0xFFFFu, inv), kv_scaled(in[2 * j + 1] >> 16, inv)) << 16);
-                    *reinterpret_cast<uint4*>(at + ((size_t)c * P + off + t) * 16) = make_uint4(out[0], out[1], out[2], out[3]);
-                }
+                        for (int j = 0; j < 4; ++j)
+                            out[j] = kv_bytes2<ODD>(in[2 * j] << 16, in[2 * j] & 0xFFFF0000u, inv) |
+                                     (kv_bytes2<ODD>(in[2 * j + 1] << 16, in[2 * j + 1] & 0xFFFF0000u, inv) << 16);
+                        *reinterpret_cast<uint4*>(at + ((size_t)c * P + off + t) * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+                    }
+                };
+                if (odd) convert(std::true_type{}); else convert(std::false_type{});
             } else {
                 // V: 16-byte groups (16 tokens of a channel), channels fastest; a group that the run fills in part
                 // keeps its other bytes
                 const unsigned short* const bits = reinterpret_cast<const unsigned short*>(rows);
-                const int g0 = moves ? 0 : off >> 4, g1 = (off + m + 15) >> 4;
-                for (int u = tid; u < (g1 - g0) * D; u += KV_COMMIT_THREADS) {
-                    const int g = g0 + u / D, d = u % D;
-                    uint8_t* const to = at + ((size_t)g * D + d) * 16;
-                    const int lo = max(16 * g, off), hi = min(16 * g + 16, off + m);   // places of the run in the group
-                    if (!moves && hi - lo < 16) {
-                        for (int t = lo; t < hi; ++t)
-                            to[t - 16 * g] = (uint8_t)kv_e4m3x2(kv_scaled(bits[(t - off) * RP + d], inv), 0.0f);
-                        continue;
-                    }
-                    uint32_t out[4] = {0, 0, 0, 0};
-                    if (hi - lo < 16) {
-                        const uint4 q = *reinterpret_cast<const uint4*>(to);
-                        const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+                const int g0 = off >> 4, g1 = (off + m + 15) >> 4;
+                auto convert = [&](auto odd_) {
+                    constexpr bool ODD = decltype(odd_)::value;
+#pragma unroll 1
+                    for (int u = tid; u < (g1 - g0) * (D / 2); u += KV_COMMIT_THREADS) {
+                        const int g = g0 + u / (D / 2), d = 2 * (u % (D / 2));             // two channels of a group
+                        const int lo = max(16 * g, off), hi = min(16 * g + 16, off + m);   // places of the run in the group
+                        if (hi - lo == 16) {
+                            const unsigned short* const from = bits + (lo - off) * RP + d;
+                            uint32_t w[16], out[8];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            // bytes in front of the run move to the new scale; those behind it stay
-                            const uint32_t mv = kv_moved(in[j], factor);
-                            const int nb = min(max(off - (16 * g + 4 * j), 0), 4);
-                            const uint32_t keep = nb == 4 ? 0xFFFFFFFFu : (1u << (8 * nb)) - 1u;
-                            out[j] = (mv & keep) | (in[j] & ~keep);
+                            for (int t = 0; t < 16; ++t) w[t] = *reinterpret_cast<const uint32_t*>(from + t * RP);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t* const v = w + 4 * j;
+                                out[j] = kv_bytes2<ODD>(v[0] << 16, v[1] << 16, inv) | (kv_bytes2<ODD>(v[2] << 16, v[3] << 16, inv) << 16);
+                                out[4 + j] = kv_bytes2<ODD>(v[0] & 0xFFFF0000u, v[1] & 0xFFFF0000u, inv) |
+                                             (kv_bytes2<ODD>(v[2] & 0xFFFF0000u, v[3] & 0xFFFF0000u, inv) << 16);
+                            }
+                            uint4* const to = reinterpret_cast<uint4*>(at + ((size_t)g * D + d) * 16);
+                            to[0] = make_uint4(out[0], out[1], out[2], out[3]);
+                            to[1] = make_uint4(out[4], out[5], out[6], out[7]);
+                            continue;
+                        }
+                        // a group that the run fills in part: its bytes one by one, the others stay
+                        uint8_t* const to = at + ((size_t)g * D + d) * 16;
+#pragma unroll 2
+                        for (int t = lo; t < hi; ++t) {
+                            const uint32_t two = *reinterpret_cast<const uint32_t*>(bits + (t - off) * RP + d);
+                            const uint32_t y = kv_bytes2<ODD>(two << 16, two & 0xFFFF0000u, inv);
+                            to[t - 16 * g] = (uint8_t)y;
+                            to[t - 16 * g + 16] = (uint8_t)(y >> 8);
                         }
                     }
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        const int place = 16 * g + t;
-                        if (place >= lo && place < hi) {
-                            const uint32_t y = kv_e4m3x2(kv_scaled(bits[(place - off) * RP + d], inv), 0.0f) & 0xFFu;
-                            out[t >> 2] = (out[t >> 2] & ~(0xFFu << (8 * (t & 3)))) | (y << (8 * (t & 3)));
-                        }
-                    }
-                    *reinterpret_cast<uint4*>(to) = make_uint4(out[0], out[1], out[2], out[3]);
-                }
+                };
+                if (odd) convert(std::true_type{}); else convert(std::false_type{});
             }
             if (tid == 0) *scale = kv_pow2(e);
             __syncthreads();   // the next run reuses the rows

@@ -1690,7 +1690,20 @@ tl_status tl_kv_slots(int* lens, const int* want, int B, int page_tokens, int* t
     if (st != TL_OK) return st;
     tl::KvSlotsParams p{lens, want, table, free_pages, n_free, slots, starts, info, B, table_width, page_log2, n_pages,
                         max_slots};
-    tl::kv_slots_kernel<<<1, tl::KV_SLOTS_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    int ctas = 1;
+    while (ctas < 8 && max_slots > tl::KV_SLOTS_A_CTA * ctas) ctas *= 2;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(tl::KV_SLOTS_THREADS);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    TL_CUDA(cudaLaunchKernelEx(&cfg, tl::kv_slots_kernel, p));
     TL_CUDA(cudaGetLastError());
     return TL_OK;
 }
@@ -1726,8 +1739,11 @@ tl_status tl_kv_commit(const tl_kv_cache* cache, const void* k, const void* v, l
     tl::KvCommitParams p{static_cast<uint8_t*>(cache->pages), cache->scales, static_cast<const __nv_bfloat16*>(k),
                          static_cast<const __nv_bfloat16*>(v), src, slots, d->err, row_stride, n_rows, n, cache->n_pages,
                          log2_of(cache->page_tokens), cache->n_kv_heads, 1};
-    // a few tokens: a CTA each, for latency; a prompt: about a page's tokens each, so that few CTAs find nothing to begin
-    p.chunk = n <= 1024 ? 1 : cache->page_tokens;
+    // a few tokens: a CTA each, for latency; more: so many that some twelve CTAs an SM remain, up to a page's tokens
+    {
+        const long long each = (long long)n * 2 * cache->n_kv_heads / (12ll * d->num_sms);
+        p.chunk = each < 1 ? 1 : each > cache->page_tokens ? cache->page_tokens : (int)each;
+    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cache->head_dim == 128 ? launch_kv_commit<128>(p, cache->page_tokens, s)
                                   : launch_kv_commit<64>(p, cache->page_tokens, s);
