@@ -8,6 +8,7 @@ library's CUDA kernels. There is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _lib
 from ._lib import Matrix, TlError, check
@@ -328,8 +329,14 @@ def kv_commit(cache, k, v, slots, src=None, stream=None):
 
 def kv_attention_workspace(cache, n_q_heads: int, batch: int, max_rows: int) -> int:
     """Bytes of workspace kv_attention() needs for these sizes."""
-    n = ctypes.c_size_t()
-    check(_lib.lib().tl_kv_attention_workspace(cache._c, n_q_heads, batch, max_rows, ctypes.byref(n)))
+    return _kv_workspace(cache.page_tokens, cache.kv_heads, cache.head_dim, n_q_heads, batch, max_rows)
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv_workspace(page_tokens, kv_heads, head_dim, n_q_heads, batch, max_rows):
+    # a function of the sizes alone
+    c, n = _lib.KvCacheC(None, None, 1, page_tokens, kv_heads, head_dim), ctypes.c_size_t()
+    check(_lib.lib().tl_kv_attention_workspace(c, n_q_heads, batch, max_rows, ctypes.byref(n)))
     return n.value
 
 
@@ -363,7 +370,7 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
         new_stride, k_ptr, v_ptr = new[1], k_new.data_ptr(), v_new.data_ptr()
     made = out is None
     if made:
-        out = torch.empty((R, hq, dim), dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty((R, hq, dim))
         out_stride = hq * dim
     else:
         n, out_stride = _rows("out", out, hq, dim, index)
@@ -373,14 +380,17 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
         return out
     own_workspace = workspace is None
     if own_workspace:
-        workspace = torch.empty(kv_attention_workspace(cache, hq, B, max_rows), dtype=torch.uint8, device=q.device)
+        size = kv_attention_workspace(cache, hq, B, max_rows)
+        workspace = q.new_empty((size + 1) // 2)      # bf16, as q is: two bytes an element
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
         _refuse(f"workspace: need a contiguous uint8 tensor on cuda:{index}")
+    else:
+        size = workspace.numel()
     _call_on(index, _lib.lib().tl_kv_attention, q.data_ptr(), q_stride, hq, cache._c, _ints("table", table, (B, width), index), width,
              _ints("lens", lens, (B,), index), B, k_ptr, v_ptr, new_stride,
              None if mask is None else _ints("mask", mask, (R,), index),
              None if row_start is None else _ints("row_start", row_start, (B + 1,), index), R, max_rows,
-             dim ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, workspace.data_ptr(), workspace.numel(),
+             dim ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, workspace.data_ptr(), size,
              _stream_of(index, stream))
     if stream is not None:   # what was allocated here for another stream than the current one
         if made:

@@ -1079,11 +1079,22 @@ template <int D>
 __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttnParams p, int chunks) {
     constexpr int E = D / 32;                            // channels of a lane
     constexpr int RP = D + 8;                            // padded row: 16-byte reads of eight rows spread over the banks
-    __shared__ __align__(16) __nv_bfloat16 kn[KV_MAX_ROWS * RP], vn[KV_MAX_ROWS * RP];
+    constexpr int LOADS = KV_MAX_ROWS * D / 8 / KV_MERGE_THREADS;     // 16-byte pieces of K a thread, and of V, at most
+    __shared__ __align__(16) __nv_bfloat16 kn[KV_MAX_ROWS * RP], vn[KV_MAX_ROWS * RP], qn[KV_MERGE_WARPS * D];
     __shared__ unsigned sums[2][KV_MERGE_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x, head = blockIdx.y / chunks, chunk = blockIdx.y % chunks;
+    // this request, and its place in the tile list
     const KvRequest rq(p, b);
+    unsigned before = 0, all = 0;
+#pragma unroll 1
+    for (int i = tid; i < p.B; i += KV_MERGE_THREADS) {
+        const KvRequest other(p, i);
+        KvShape sh(other.rows * p.group, kv_tiles(other.len), p.nt);
+        const unsigned w = other.len > 0 ? (unsigned)(p.heads * sh.row_tiles) * sh.unit_w : 0u;
+        all += w;
+        if (i < b) before += w;
+    }
     const int first = rq.first, rows = rq.rows;
     if (rq.bad && tid == 0 && blockIdx.y == 0) atomicCAS(p.err, 0, TL_DEV_ERR_KV_ROWS);
     // every CTA waits for the streaming kernel, so that this launch never ends before it
@@ -1091,53 +1102,60 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
+    const int r = chunk * KV_MERGE_WARPS + warp, i = r / p.group, h = head * p.group + r % p.group;
+    const int row = first + i;
+    const bool works = r < rows * p.group;
+    unsigned bits = 0;
     if (p.k_new) {
-        for (int e = tid; e < rows * (D / 8); e += KV_MERGE_THREADS) {
-            const int j = e / (D / 8), c = e % (D / 8);
-            const size_t at = (size_t)(first + j) * p.new_stride + (size_t)head * D + 8 * c;
-            *reinterpret_cast<uint4*>(kn + j * RP + 8 * c) = __ldg(reinterpret_cast<const uint4*>(p.k_new + at));
-            *reinterpret_cast<uint4*>(vn + j * RP + 8 * c) = __ldg(reinterpret_cast<const uint4*>(p.v_new + at));
+        // all that the tree's part reads, in one go
+        uint4 kq[LOADS], vq[LOADS], qq = make_uint4(0, 0, 0, 0);
+        const size_t base = (size_t)first * p.new_stride + (size_t)head * D;
+#pragma unroll
+        for (int u = 0; u < LOADS; ++u) {
+            const int e = tid + u * KV_MERGE_THREADS, j = e / (D / 8), c = e % (D / 8);
+            if (j < rows) {
+                kq[u] = __ldg(reinterpret_cast<const uint4*>(p.k_new + base + (size_t)j * p.new_stride + 8 * c));
+                vq[u] = __ldg(reinterpret_cast<const uint4*>(p.v_new + base + (size_t)j * p.new_stride + 8 * c));
+            }
         }
-    }
-    // this request's place in the tile list
-    unsigned before = 0, all = 0;
-#pragma unroll 1
-    for (int i = tid; i < p.B; i += KV_MERGE_THREADS) {
-        const KvRequest other(p, i);
-        const KvShape sh(other.rows * p.group, kv_tiles(other.len), p.nt);
-        const unsigned w = other.len > 0 ? (unsigned)(p.heads * sh.row_tiles) * sh.unit_w : 0u;
-        all += w;
-        if (i < b) before += w;
+        if (works) {
+            if (lane < D / 8) qq = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)row * p.q_stride + (size_t)h * D) + lane);
+            bits = p.mask ? __ldg(p.mask + row) : (2u << i) - 1u;
+            if (rows < 32) bits &= (1u << rows) - 1u;
+        }
+#pragma unroll
+        for (int u = 0; u < LOADS; ++u) {
+            const int e = tid + u * KV_MERGE_THREADS, j = e / (D / 8), c = e % (D / 8);
+            if (j < rows) {
+                *reinterpret_cast<uint4*>(kn + j * RP + 8 * c) = kq[u];
+                *reinterpret_cast<uint4*>(vn + j * RP + 8 * c) = vq[u];
+            }
+        }
+        if (lane < D / 8) *reinterpret_cast<uint4*>(qn + warp * D + 8 * lane) = qq;
     }
     all = __reduce_add_sync(0xFFFFFFFFu, all);
     before = __reduce_add_sync(0xFFFFFFFFu, before);
     if (lane == 0) { sums[0][warp] = all; sums[1][warp] = before; }
     __syncthreads();
-    all = before = 0;
-#pragma unroll
-    for (int u = 0; u < KV_MERGE_WARPS; ++u) { all += sums[0][u]; before += sums[1][u]; }
-    const int r = chunk * KV_MERGE_WARPS + warp;
-    if (r >= rows * p.group) {
+    if (!works) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
-    const int i = r / p.group, h = head * p.group + r % p.group;
-    const int row = first + i;
+    all = before = 0;
+#pragma unroll
+    for (int u = 0; u < KV_MERGE_WARPS; ++u) { all += sums[0][u]; before += sums[1][u]; }
 
     float m = -INFINITY, l = 0.0f;
     float o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    if (p.k_new) {
-        unsigned bits = p.mask ? p.mask[row] : (2u << i) - 1u;
-        if (rows < 32) bits &= (1u << rows) - 1u;
+    if (bits) {
         const bool sees = (bits >> lane) & 1u;
-        const uint4* const qr = reinterpret_cast<const uint4*>(p.q + (size_t)row * p.q_stride + (size_t)h * D);
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (sees) {
-#pragma unroll 4
+#pragma unroll 8
             for (int c = 0; c < D / 8; ++c) {
-                const uint4 a = *reinterpret_cast<const uint4*>(kn + lane * RP + 8 * c), w = __ldg(qr + c);
+                const uint4 a = *reinterpret_cast<const uint4*>(kn + lane * RP + 8 * c), w = *reinterpret_cast<const uint4*>(qn + warp * D + 8 * c);
                 const uint32_t ka[4] = {a.x, a.y, a.z, a.w}, qa[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
@@ -1146,25 +1164,28 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
             }
         }
         const float s = sees ? ((acc[0] + acc[1]) + (acc[2] + acc[3])) * p.scale : -INFINITY;
-        const float top = kv_warp_max(s);
-        const float pr = sees ? exp2f(s - top) : 0.0f;
-        float sum = pr;
+        m = kv_warp_max(s);
+        const float pr = sees ? exp2f(s - m) : 0.0f;
+        l = pr;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if (bits) { m = top; l = sum; }
-        for (unsigned todo = bits; todo; todo &= todo - 1) {
-            const int j = __ffs(todo) - 1;
-            const float w = __shfl_sync(0xFFFFFFFFu, pr, j);
+        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+        for (unsigned todo = bits; todo;) {
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const uint32_t x = *reinterpret_cast<const uint32_t*>(vn + j * RP + E * lane + e);
-                o[e] = fmaf(w, __int_as_float((int)(x << 16)), o[e]);
-                o[e + 1] = fmaf(w, __int_as_float((int)(x & 0xFFFF0000u)), o[e + 1]);
+            for (int u = 0; u < 4; ++u) {
+                const int j = todo ? __ffs(todo) - 1 : 0;
+                const float w = todo ? __shfl_sync(0xFFFFFFFFu, pr, j) : 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const uint32_t x = todo ? *reinterpret_cast<const uint32_t*>(vn + j * RP + E * lane + e) : 0u;
+                    o[e] = fmaf(w, __int_as_float((int)(x << 16)), o[e]);
+                    o[e + 1] = fmaf(w, __int_as_float((int)(x & 0xFFFF0000u)), o[e + 1]);
+                }
+                todo &= todo - 1;
             }
         }
     }
     // the parts of the cached tokens: a lane looks at a part (whether the CTA had a tile of the unit, and its m and l), then
-    // all lanes add the parts' O in order, eight loads in flight
+    // all lanes add the parts' O in order, eight loads in flight, the first eight beside those of m and l
     const int tiles = kv_tiles(rq.len);
     const KvShape sh(rows * p.group, tiles, p.nt);
     const int rt = r / sh.nt, n = r - rt * sh.nt;
@@ -1176,7 +1197,7 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
         g0 = shares.owner(at0);
         g1 = shares.owner(at0 + sh.unit_w - 1);
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool waits = true;
     for (int gb = g0; gb <= g1; gb += 32) {
         const int g = gb + lane;
         float2 ml = make_float2(-INFINITY, 0.0f);
@@ -1184,42 +1205,52 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
         if (g <= g1) {
             const unsigned lo = shares.start(g), hi = shares.start(g + 1);
             has = sh.tile_from(lo > at0 ? lo - at0 : 0u, tiles) < sh.tile_from(hi > at0 ? hi - at0 : 0u, tiles);
-            if (has) ml = __ldcg(p.part_ml + (size_t)(slot0 + g) * p.nt + n);
         }
-        const float top = fmaxf(m, kv_warp_max(ml.x));
-        // a part or tree without weight (m of minus infinity) counts nothing, but a NaN of it counts
-        const float f0 = (m == -INFINITY) ? 0.0f : exp2f(m - top), f = (ml.x == -INFINITY) ? 0.0f : exp2f(ml.x - top);
-        float sum = ml.y * f;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        m = top;
-        l = l * f0 + sum;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= f0;
         unsigned todo = __ballot_sync(0xFFFFFFFFu, has);
+        if (waits) asm volatile("griddepcontrol.wait;" ::: "memory");
+        waits = false;
+        if (has) ml = __ldcg(p.part_ml + (size_t)(slot0 + g) * p.nt + n);
+        float f = 0.0f;
+        bool fresh = true;
         while (todo) {
             float2 x[8][E / 2];
-            float fs[8];
+            unsigned left = todo;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const int src = todo ? __ffs(todo) - 1 : 0;
-                fs[u] = todo ? __shfl_sync(0xFFFFFFFFu, f, src) : 0.0f;
+                const int src = left ? __ffs(left) - 1 : 0;
 #pragma unroll
                 for (int e = 0; e < E; e += 2)
-                    x[u][e / 2] = todo ? __ldcg(reinterpret_cast<const float2*>(p.part_o + ((size_t)(slot0 + gb + src) * p.nt + n) * D + E * lane + e))
+                    x[u][e / 2] = left ? __ldcg(reinterpret_cast<const float2*>(p.part_o + ((size_t)(slot0 + gb + src) * p.nt + n) * D + E * lane + e))
                                        : make_float2(0.0f, 0.0f);
-                todo &= todo - 1;
+                left &= left - 1;
+            }
+            if (fresh) {
+                const float top = fmaxf(m, kv_warp_max(ml.x));
+                // a part or tree without weight (m of minus infinity) counts nothing, but a NaN of it counts
+                const float f0 = (m == -INFINITY) ? 0.0f : exp2f(m - top);
+                f = (ml.x == -INFINITY) ? 0.0f : exp2f(ml.x - top);
+                float sum = ml.y * f;
+#pragma unroll
+                for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+                m = top;
+                l = l * f0 + sum;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] *= f0;
+                fresh = false;
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
+                const float fu = todo ? __shfl_sync(0xFFFFFFFFu, f, __ffs(todo) - 1) : 0.0f;
 #pragma unroll
                 for (int e = 0; e < E; e += 2) {
-                    o[e] = fmaf(x[u][e / 2].x, fs[u], o[e]);
-                    o[e + 1] = fmaf(x[u][e / 2].y, fs[u], o[e + 1]);
+                    o[e] = fmaf(x[u][e / 2].x, fu, o[e]);
+                    o[e + 1] = fmaf(x[u][e / 2].y, fu, o[e + 1]);
                 }
+                todo &= todo - 1;
             }
         }
     }
+    if (waits) asm volatile("griddepcontrol.wait;" ::: "memory");
     const float inv = (m == -INFINITY && l == 0.0f) ? 0.0f : 1.0f / l;
     __nv_bfloat16* const to = p.out + (size_t)row * p.out_stride + (size_t)h * D + E * lane;
 #pragma unroll
