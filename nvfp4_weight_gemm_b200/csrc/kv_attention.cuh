@@ -81,8 +81,10 @@ struct KvRequest {
 
 __device__ __forceinline__ int kv_tiles(int len) { return (int)(((unsigned)len + KV_TILE - 1) / KV_TILE); }
 
-// Weights, in about 200 cycles: a tile's share that does not depend on its rows, and a unit's beginning and end.
-constexpr int KV_W_TILE = 4, KV_W_UNIT = 12;
+// Weights, in about 350 cycles: a tile's share that does not depend on its rows, and a unit's beginning and end. (Of 6, 9,
+// 12, 16 and 22 for the latter: 24 requests of about 3k tokens in 34.8, 33.2, 31.0, 31.2 and 32.7 us,
+// a mix of long and short ones in 74, 69, 62, 51 and 52.)
+constexpr int KV_W_TILE = 4, KV_W_UNIT = 16;
 
 // How the rows of a request are cut for row tiles of at most `most` rows, and what its units weigh. (The host keeps the
 // weight of a whole call below 2^32.)
@@ -191,9 +193,9 @@ struct KvWalk {
 //     S^T [token][row]   = K  [token][channel] . Q^T      E4M3: A = the cache's bytes, moved to tensor memory as they are
 //     O^T [channel][row] = V^T [channel][token] . P^T     f16:  A = V in tensor memory,  B = P in shared memory
 //
-// K is never converted: Q is. (K fed from shared memory would need a tile's pages in pieces of 16 channels, and bulk copies
-// that small, 18 a tile, took the decode case from 140 to 172 us.) Each row of Q is scaled by a power of two that brings its largest magnitude into
-// (224, 448] and written as the sum of two E4M3 terms, the second holding what the first left over. A bf16 value
+// K is never converted: Q is. (Operand A in shared memory would have to have K's 128 tokens side by side: a tile's pages in
+// pieces of 16 channels, and bulk copies that small, 18 a tile, were 23% slower for one row than moving K from whole pages.)
+// Each row of Q is scaled by a power of two that brings its largest magnitude into (224, 448] and written as the sum of two E4M3 terms, the second holding what the first left over. A bf16 value
 // has 8 significant bits and a term holds 4, so the sum is exact for elements down to 2^-10 of the largest; the
 // others are within 2^-10 in that scale, 2^-17.8 of the row's largest. Both terms multiply the same K into one fp32
 // accumulator (products of E4M3 are exact in it).
@@ -210,14 +212,19 @@ struct KvWalk {
 //                   other roles follow (the walk in every role was code of 8 KB each, and instruction fetches a bound);
 //                   producer: a page's K and V of the head are one contiguous piece, brought in by one bulk copy;
 //                   tiles of 128 tokens, a ring of stages. Scales follow by cp.async.
-//   * warp 1        issues the MMAs of S^T, warp 2 those of O^T (an issuer manages one MMA in some 55 cycles while
-//                   other warps run, so one warp for all sixteen of a tile was a bound).
+//   * warp 1        issues the MMAs of S^T, warp 2 those of O^T (each waits for other roles).
 //   * warp 3        the rows: Q of the next segment to one of two buffers in shared memory. The first segment's Q is
 //                   brought in by the softmax warps, which have nothing to do yet.
 //   * warps 4..7    movers: K (lane = token), then V, converted (lane = channel), 16 bytes of a lane at a time.
 //   * warps 8..15   softmax: two groups of four warps, half of the blocks of 8 rows each, lane = token; blocks without
 //                   rows are passed over. A group also reads its rows of O (lane = channel) when a segment ends and writes
 //                   the part.
+// Bound: for a few rows the cache's bytes (64 requests of up to 8k tokens, 8 KV heads of 128, one row each: 106 us, 80% of
+// what a copy reaches). A tile of 128 tokens and 128 channels takes 1,580 cycles with 16 rows, 2,300 with 48 and 3,430 with
+// 80, of which memory needs 1,460 (one row tile); with many rows it is the softmax's chain of waits, loads, exponentials
+// (640 cycles of their unit at 80 rows), stores and votes, while no unit is busy half the time. Rows as operand A, padded
+// to 128 and a row a thread (no votes, no exchange across lanes), took 3,550; the groups on alternate tiles, four groups on
+// two tiles, or three groups on thirds of the rows took 3,900 and more.
 // Every mbarrier wait is bounded; after one has run out the others return at once, every role runs to its end
 // (so no named barrier is left waiting), and the status word is set.
 
@@ -1071,8 +1078,9 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
 // One warp per row of a unit, a CTA's rows all of one unit, so that they share the tree's K and V of the KV head in
 // shared memory: the scores of the nodes that the row sees (a lane a node), their softmax and V in fp32, then the
 // parts of the cached tokens, in list order. What the mask leaves out is never used, so nothing of it (an infinity, a
-// NaN) reaches the row. A row that sees nothing at all gives zeros. Latency-bound: all of it up to the parts runs
-// while the streaming kernel does.
+// NaN) reaches the row. A row that sees nothing at all gives zeros. Latency-bound, so all loads that do not depend on one
+// another are in flight at once. It is launched early, but the streaming kernel has all registers of an SM: the tree's part
+// runs while other SMs still stream.
 constexpr int KV_MERGE_WARPS = 8, KV_MERGE_THREADS = 32 * KV_MERGE_WARPS;
 
 template <int D>

@@ -1776,7 +1776,7 @@ tl_status tl_kv_attention(const void* q, long long q_stride, int n_q_heads, cons
     {
         const long long tiles = ((long long)table_width * cache->page_tokens + 127) / 128;
         const int row_tiles = (max_rows * (n_q_heads / cache->n_kv_heads) + 79) / 80;
-        if ((double)B * cache->n_kv_heads * row_tiles * (12.0 + 9.0 * (double)tiles) > 4.0e9)
+        if ((double)B * cache->n_kv_heads * row_tiles * (tl::KV_W_UNIT + 9.0 * (double)tiles) > 4.0e9)
             return fail(TL_ERR_UNSUPPORTED, "B * n_kv_heads * table_width is too large for one call: give fewer requests");
     }
     if (R < 0 || (!row_start && R != B * max_rows))
