@@ -115,6 +115,17 @@ def test_slots_many_tokens_share_the_work_of_several_blocks():
     assert _check_slots(ref[0], lens, 16, ref[1], ref[2], ref[3], 40000)[1][6] == [0, 0, 0, 0]
 
 
+@pytest.mark.parametrize("room", [1, 2047, 2048, 2049, 4097, 8193, 9001])
+def test_slots_of_every_number_of_blocks(room):
+    # the arrays' room sets how many blocks deal the slots out, whether they are filled or not
+    rs = np.random.default_rng(room)
+    lens, table, free, n = _slots_state(rs, 70, 32, 200, spare=2000, width_spare=200)
+    want = lens + rs.integers(0, 5, 70)
+    want[5] += max(0, room - int((want - lens).sum()) - int(rs.integers(0, 3)))
+    want[9] = 0
+    _check_slots(lens, want, 32, table, free, n, room)
+
+
 def test_slots_refuse_and_leave():
     table, free = np.array([[0, -1, -1], [1, -1, -1]]), np.array([2, 9, 9, 9])
     for lens, want, n, room in (([16, 16], [32, 32], 1, 99), ([16, 16], [18, 8], 1, 1), ([16, 16], [49, 18], 1, 9),
@@ -194,6 +205,28 @@ def test_commit_long_prompts_take_the_page_chunks():
             at += -(-(o + m) // P)
         n = len(slots)
         _check_commit(pages, scales, P, rs.normal(0, 1, (n, 1, 64)), rs.normal(0, 1, (n, 1, 64)), slots)
+
+
+@pytest.mark.parametrize("P,H,D,n", [(16, 8, 64, 330), (64, 8, 128, 450), (64, 16, 64, 900), (128, 4, 128, 1500)])
+def test_commit_short_runs_of_which_a_block_writes_several(P, H, D, n):
+    # requests of 1 to 20 tokens behind none or some, of magnitudes far apart (scales grow), a few values not finite
+    rs = np.random.default_rng(P + n)
+    n_pages = 2 * n // P + n // 4 + 8
+    pages, scales = _rand_pool(rs, n_pages, H, P, D)
+    ids, slots, size, at = rs.permutation(n_pages), [], [], 0
+    while len(slots) < n:
+        pos = int(rs.integers(0, P)) * int(rs.integers(0, 2)) + np.arange(int(rs.integers(1, 21)))
+        if at + pos[-1] // P >= n_pages:
+            break
+        slots += list(ids[at + pos // P] * P + pos % P)
+        size += [2.0 ** int(rs.integers(-9, 9))] * len(pos)
+        at += pos[-1] // P + 1
+    m = len(slots)
+    k, v = rs.normal(0, 1, (2, m, H, D)) * np.array(size)[None, :, None, None]
+    for x in (k, v):
+        for value in (np.nan, np.inf, -np.inf):
+            x[rs.integers(0, m, 5), rs.integers(0, H, 5), rs.integers(0, D, 5)] = value
+    _check_commit(pages, scales, P, k, v, np.array(slots))
 
 
 @pytest.mark.parametrize("P", [16, 64])

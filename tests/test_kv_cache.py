@@ -94,6 +94,14 @@ def test_attention_refuses(L):
     assert "overlap" in L.tl_last_error_message().decode()
 
 
+def test_attention_refuses_more_work_than_it_counts_in_32_bits(L):
+    # 1024 requests x 8 KV heads x 7 tiles of 80 rows, each of 16 + 9 a tile of 128 tokens, at most 4e9 in all: 7748 tiles
+    for tiles, code in ((7748, 1), (7749, 3)):
+        assert L.tl_kv_attention(_at(2), 128 * 128, 128, ctypes.byref(_cache()), _at(3), 2 * tiles, _at(4), 1024, None, None, 0, None,
+                                 _at(8), 100, 32, ctypes.c_float(0.1), _at(9), 128 * 128, _at(10), 16, None) == code
+    assert "too large for one call" in L.tl_last_error_message().decode()
+
+
 def test_workspace_grows_with_its_sizes(L):
     def need(hq, B, rows, **kw):
         n = ctypes.c_size_t()
