@@ -219,7 +219,8 @@ def gdn_commit(state, k, v, alpha, beta, path, stream=None):
 # ---------------------------------------------------------------- 8-bit paged KV cache
 #
 # What the library cannot see behind a pointer (types, shapes, devices) is checked here, with few Python
-# operations: these calls come every decoding round.
+# operations: these calls come every decoding round, and a call of a few tokens is bound by the host. So
+# the tensors are looked at together, and one by one only to say which is wrong.
 
 def _refuse(what: str):
     raise ValueError(what)
@@ -251,14 +252,21 @@ def _stream_of(index, stream):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _call_on(index, fn, *args):
+def _call_on(index, fn, args):
     """fn(*args) with CUDA device `index` current."""
     import torch
     if torch._C._cuda_getDevice() == index:
-        check(fn(*args))
+        status = fn(*args)
     else:
         with torch.cuda.device(index):
-            check(fn(*args))
+            status = fn(*args)
+    if status:
+        check(status)
+
+
+def _same_rows(a, b):
+    """Whether b has a's type, device, shape and strides."""
+    return a.dtype is b.dtype and a.shape == b.shape and a.stride() == b.stride() and a.get_device() == b.get_device()
 
 
 class KvCache:
@@ -301,14 +309,27 @@ def kv_slots(lens, want, table, free_pages, n_free, page_tokens, slots, starts, 
     slots [max_slots] (a slot for every token that requests grow by, then -1), starts [B + 1], info [4]
     (code, pages missing, slots missing, requests refused). lens, table, free_pages and n_free are updated in place.
     Returns (slots, starts, info)."""
-    index = lens.get_device()
+    import torch
+    index, i32 = lens.get_device(), torch.int32
     if index < 0 or lens.dim() != 1:
         _refuse("lens: need an int32 tensor [B] on a CUDA device")
-    B, width, n_pages, room = lens.shape[0], table.shape[-1], free_pages.numel(), slots.numel()
-    _call_on(index, _lib.lib().tl_kv_slots, _ints("lens", lens, (B,), index), _ints("want", want, (B,), index), B, page_tokens,
-             _ints("table", table, (B, width), index), width, _ints("free_pages", free_pages, (n_pages,), index), n_pages,
-             _ints("n_free", n_free, (1,), index), _ints("slots", slots, (room,), index), room,
-             _ints("starts", starts, (B + 1,), index), _ints("info", info, (4,), index), _stream_of(index, stream))
+    B, width, n_pages, room = lens.numel(), table.shape[-1], free_pages.numel(), slots.numel()
+    if not (lens.dtype is i32 and want.dtype is i32 and table.dtype is i32 and free_pages.dtype is i32 and n_free.dtype is i32
+            and slots.dtype is i32 and starts.dtype is i32 and info.dtype is i32
+            and want.get_device() == index and table.get_device() == index and free_pages.get_device() == index
+            and n_free.get_device() == index and slots.get_device() == index and starts.get_device() == index
+            and info.get_device() == index
+            and want.shape == lens.shape and table.shape == (B, width) and free_pages.dim() == 1 and n_free.shape == (1,)
+            and slots.dim() == 1 and starts.shape == (B + 1,) and info.shape == (4,)
+            and lens.is_contiguous() and want.is_contiguous() and table.is_contiguous() and free_pages.is_contiguous()
+            and n_free.is_contiguous() and slots.is_contiguous() and starts.is_contiguous() and info.is_contiguous()):
+        for name, t, shape in (("lens", lens, (B,)), ("want", want, (B,)), ("table", table, (B, width)),
+                               ("free_pages", free_pages, (n_pages,)), ("n_free", n_free, (1,)), ("slots", slots, (room,)),
+                               ("starts", starts, (B + 1,)), ("info", info, (4,))):
+            _ints(name, t, shape, index)
+    _call_on(index, _lib.lib().tl_kv_slots,
+             (lens.data_ptr(), want.data_ptr(), B, page_tokens, table.data_ptr(), width, free_pages.data_ptr(), n_pages,
+              n_free.data_ptr(), slots.data_ptr(), room, starts.data_ptr(), info.data_ptr(), _stream_of(index, stream)))
     return slots, starts, info
 
 
@@ -319,11 +340,12 @@ def kv_commit(cache, k, v, slots, src=None, stream=None):
     kv_slots() writes them (negative: nowhere); src int32 [n] or None. Returns `cache`."""
     index = cache._on_gpu()
     rows = _rows("k", k, cache.kv_heads, cache.head_dim, index)
-    if _rows("v", v, cache.kv_heads, cache.head_dim, index) != rows:
+    if not _same_rows(k, v) and _rows("v", v, cache.kv_heads, cache.head_dim, index) != rows:
         _refuse("k and v must have the same rows and row stride")
     n = slots.numel()
-    _call_on(index, _lib.lib().tl_kv_commit, cache._c, k.data_ptr(), v.data_ptr(), rows[1], rows[0],
-             None if src is None else _ints("src", src, (n,), index), _ints("slots", slots, (n,), index), n, _stream_of(index, stream))
+    _call_on(index, _lib.lib().tl_kv_commit,
+             (cache._c, k.data_ptr(), v.data_ptr(), rows[1], rows[0], None if src is None else _ints("src", src, (n,), index),
+              _ints("slots", slots, (n,), index), n, _stream_of(index, stream)))
     return cache
 
 
@@ -365,7 +387,7 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
         if k_new is None or v_new is None:
             _refuse("k_new and v_new go together")
         new = _rows("k_new", k_new, heads, dim, index)
-        if new[0] != R or _rows("v_new", v_new, heads, dim, index) != new:
+        if new[0] != R or (not _same_rows(k_new, v_new) and _rows("v_new", v_new, heads, dim, index) != new):
             _refuse("k_new and v_new must have q's rows and one row stride")
         new_stride, k_ptr, v_ptr = new[1], k_new.data_ptr(), v_new.data_ptr()
     made = out is None
@@ -386,12 +408,17 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
         _refuse(f"workspace: need a contiguous uint8 tensor on cuda:{index}")
     else:
         size = workspace.numel()
-    _call_on(index, _lib.lib().tl_kv_attention, q.data_ptr(), q_stride, hq, cache._c, _ints("table", table, (B, width), index), width,
-             _ints("lens", lens, (B,), index), B, k_ptr, v_ptr, new_stride,
-             None if mask is None else _ints("mask", mask, (R,), index),
-             None if row_start is None else _ints("row_start", row_start, (B + 1,), index), R, max_rows,
-             dim ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, workspace.data_ptr(), size,
-             _stream_of(index, stream))
+    i32 = torch.int32
+    if not (table.dtype is i32 and lens.dtype is i32 and table.shape == (B, width) and lens.dim() == 1
+            and table.get_device() == index and lens.get_device() == index and table.is_contiguous() and lens.is_contiguous()):
+        _ints("table", table, (B, width), index)
+        _ints("lens", lens, (B,), index)
+    _call_on(index, _lib.lib().tl_kv_attention,
+             (q.data_ptr(), q_stride, hq, cache._c, table.data_ptr(), width, lens.data_ptr(), B, k_ptr, v_ptr, new_stride,
+              None if mask is None else _ints("mask", mask, (R,), index),
+              None if row_start is None else _ints("row_start", row_start, (B + 1,), index), R, max_rows,
+              dim ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, workspace.data_ptr(), size,
+              _stream_of(index, stream)))
     if stream is not None:   # what was allocated here for another stream than the current one
         if made:
             out.record_stream(stream)

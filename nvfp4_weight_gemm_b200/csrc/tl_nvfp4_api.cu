@@ -1286,8 +1286,7 @@ tl_status check_kv_heads(const tl_kv_cache& c, int n_q_heads, int B, int max_row
 
 template <int D>
 tl_status launch_kv_commit(const tl::KvCommitParams& p, int page_tokens, cudaStream_t stream) {
-    const int smem = page_tokens * (D + 8) * 2;
-    TL_CUDA(cudaFuncSetAttribute(tl::kv_commit_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * (D + 8) * 2));
+    const int smem = page_tokens * (D + 8) * 2;      // 34 KB at most
     const dim3 grid((unsigned)((p.n + p.chunk - 1) / p.chunk), (unsigned)(2 * p.heads));
     tl::kv_commit_kernel<D><<<grid, tl::KV_COMMIT_THREADS, smem, stream>>>(p);
     TL_CUDA(cudaGetLastError());

@@ -646,3 +646,46 @@ def test_a_served_batch_round_by_round():
     used = h["table"][h["table"] >= 0]
     assert np.array_equal(cache.scales.cpu().numpy()[used], h["scales"][used])
     assert np.array_equal(got[used], h["pages"][used])
+
+
+def _wrong(t):
+    """Tensors that differ from t in one thing: type, layout, shape, device."""
+    twice = torch.stack([t, t], -1)
+    out = [t.float() if t.dtype is torch.int32 else t.half(), t[None], t.cpu()]
+    if t.numel() > 1:                                       # one element is contiguous whatever its stride
+        out += [twice[..., 0], t[:-1]]
+    return out
+
+
+def test_binding_refuses_wrong_tensors():
+    i = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=DEV)  # noqa: E731
+    good = dict(lens=i(3), want=i(3), table=i(3, 2), free_pages=i(6), n_free=i(1), slots=i(9), starts=i(4), info=i(4))
+    tl.kv_slots(page_tokens=16, **good)
+    for name, t in good.items():
+        for k, bad in enumerate(_wrong(t)):
+            if k == 4 and name in ("free_pages", "slots"):
+                continue                                    # any length will do
+            with pytest.raises(ValueError):
+                tl.kv_slots(page_tokens=16, **{**good, name: bad})
+    x = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    cache = tl.KvCache(torch.zeros((6, 2, 2, 1024), dtype=torch.uint8, device=DEV), torch.ones((6, 2, 2), device=DEV), 16)
+    good = dict(k=x(5, 2, 64), v=x(5, 2, 64), slots=i(5) - 1)
+    tl.kv_commit(cache, **good)
+    for name, t in good.items():
+        for k, bad in enumerate(_wrong(t)):
+            if not (k == 4 and name == "slots"):            # fewer slots than rows will do
+                with pytest.raises(ValueError):
+                    tl.kv_commit(cache, **{**good, name: bad})
+    good = dict(q=x(5, 4, 64), table=i(2, 3), lens=i(2), k_new=x(5, 2, 64), v_new=x(5, 2, 64), mask=i(5), row_start=i(3), out=x(5, 4, 64))
+    tl.kv_attention(cache=cache, max_rows=4, **good)
+    for name, t in good.items():
+        for bad in _wrong(t):
+            with pytest.raises(ValueError):
+                tl.kv_attention(cache=cache, max_rows=4, **{**good, name: bad})
+    with pytest.raises(ValueError):
+        tl.kv_attention(cache=cache, max_rows=4, workspace=x(99999), **good)
+    # one row: its stride says nothing, and need not agree
+    one = dict(q=x(1, 4, 64), table=i(1, 3), lens=i(1), k_new=x(2, 2, 64)[:1], v_new=x(1, 4, 64)[:, :2], out=x(1, 4, 64))
+    tl.kv_attention(cache=cache, **one)
+    torch.cuda.synchronize()
+    tl.check_device_error()
