@@ -81,7 +81,7 @@ struct KvRequest {
 
 __device__ __forceinline__ int kv_tiles(int len) { return (int)(((unsigned)len + KV_TILE - 1) / KV_TILE); }
 
-// Weights, in about 350 cycles: a tile's share that does not depend on its rows, and a unit's beginning and end. (Of 6, 9,
+// Weights, in about 0.18 us: a tile's share that does not depend on its rows, and a unit's beginning and end. (Of 6, 9,
 // 12, 16 and 22 for the latter: 24 requests of about 3k tokens in 34.8, 33.2, 31.0, 31.2 and 32.7 us,
 // a mix of long and short ones in 74, 69, 62, 51 and 52.)
 constexpr int KV_W_TILE = 4, KV_W_UNIT = 16;
@@ -220,11 +220,12 @@ struct KvWalk {
 //                   rows are passed over. A group also reads its rows of O (lane = channel) when a segment ends and writes
 //                   the part.
 // Bound: for a few rows the cache's bytes (64 requests of up to 8k tokens, 8 KV heads of 128, one row each: 106 us, 80% of
-// what a copy reaches). A tile of 128 tokens and 128 channels takes 1,580 cycles with 16 rows, 2,300 with 48 and 3,430 with
-// 80, of which memory needs 1,460 (one row tile); with many rows it is the softmax's chain of waits, loads, exponentials
-// (640 cycles of their unit at 80 rows), stores and votes, while no unit is busy half the time. Rows as operand A, padded
-// to 128 and a row a thread (no votes, no exchange across lanes), took 3,550; the groups on alternate tiles, four groups on
-// two tiles, or three groups on thirds of the rows took 3,900 and more.
+// what a copy reaches). A tile of 128 tokens and 128 channels takes 0.82 us with 16 rows, 1.17 with 48 and 1.72 with 80, of
+// which memory needs 0.74. With many rows it is the softmax's: its warps are busy all the time, one step after another (a
+// thread's 40 scores of a tile: 150 ns of load and wait for them, 250 of scale and maximum, 100 of vote, 250 to 400 of
+// exponentials, 70 of fence and arrival, 130 of the next tile's wait), and no unit is busy half the time. Rows as operand A,
+// padded to 128 and a row a thread (no votes, no exchange across lanes), took 1.81; the groups on alternate tiles, four groups
+// on two tiles, or three groups on thirds of the rows 1.99 and more.
 // Every mbarrier wait is bounded; after one has run out the others return at once, every role runs to its end
 // (so no named barrier is left waiting), and the status word is set.
 
