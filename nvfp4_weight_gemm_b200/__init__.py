@@ -284,7 +284,7 @@ class KvCache:
         n, heads, _, side = shape
         if page_tokens <= 0 or side % page_tokens:
             _refuse("pages: page_tokens does not divide a page's side")
-        if scales.dtype is not torch.float32 or scales.shape != shape[:3] or not scales.is_contiguous() or scales.device != pages.device:
+        if scales.dtype is not torch.float32 or scales.shape != shape[:3] or not scales.is_contiguous() or scales.get_device() != pages.get_device():
             _refuse("scales: need a contiguous float32 tensor [n_pages, kv_heads, 2] beside pages")
         self.pages, self.scales, self.page_tokens = pages, scales, page_tokens
         self.n_pages, self.kv_heads, self.head_dim, self.index = n, heads, side // page_tokens, pages.get_device()
@@ -373,7 +373,7 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
     (None: R / B rows each). scale defaults to head_dim ** -0.5. out bf16 [R, q_heads, head_dim]; workspace uint8 of
     kv_attention_workspace() bytes (both allocated when None). Returns `out`."""
     import torch
-    index, heads, dim = cache._on_gpu(), cache.kv_heads, cache.head_dim
+    index, heads, dim, i32 = cache._on_gpu(), cache.kv_heads, cache.head_dim, torch.int32
     hq = q.shape[1] if q.dim() == 3 else -1
     R, q_stride = _rows("q", q, hq, dim, index)
     B, width = lens.numel(), table.shape[-1]
@@ -392,7 +392,7 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
         new_stride, k_ptr, v_ptr = new[1], k_new.data_ptr(), v_new.data_ptr()
     made = out is None
     if made:
-        out = q.new_empty((R, hq, dim))
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((R, hq, dim))
         out_stride = hq * dim
     else:
         n, out_stride = _rows("out", out, hq, dim, index)
@@ -408,16 +408,22 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
         _refuse(f"workspace: need a contiguous uint8 tensor on cuda:{index}")
     else:
         size = workspace.numel()
-    i32 = torch.int32
+    mask_ptr = start_ptr = None
     if not (table.dtype is i32 and lens.dtype is i32 and table.shape == (B, width) and lens.dim() == 1
             and table.get_device() == index and lens.get_device() == index and table.is_contiguous() and lens.is_contiguous()):
         _ints("table", table, (B, width), index)
         _ints("lens", lens, (B,), index)
+    if mask is not None:
+        if not (mask.dtype is i32 and mask.shape == (R,) and mask.get_device() == index and mask.is_contiguous()):
+            _ints("mask", mask, (R,), index)
+        mask_ptr = mask.data_ptr()
+    if row_start is not None:
+        if not (row_start.dtype is i32 and row_start.shape == (B + 1,) and row_start.get_device() == index and row_start.is_contiguous()):
+            _ints("row_start", row_start, (B + 1,), index)
+        start_ptr = row_start.data_ptr()
     _call_on(index, _lib.lib().tl_kv_attention,
              (q.data_ptr(), q_stride, hq, cache._c, table.data_ptr(), width, lens.data_ptr(), B, k_ptr, v_ptr, new_stride,
-              None if mask is None else _ints("mask", mask, (R,), index),
-              None if row_start is None else _ints("row_start", row_start, (B + 1,), index), R, max_rows,
-              dim ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, workspace.data_ptr(), size,
+              mask_ptr, start_ptr, R, max_rows, dim ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, workspace.data_ptr(), size,
               _stream_of(index, stream)))
     if stream is not None:   # what was allocated here for another stream than the current one
         if made:

@@ -80,6 +80,7 @@ struct DevState {
     unsigned* counters = nullptr;  // [8 * num_sms]: four per split, up to 2 * num_sms splits
     unsigned* qscratch = nullptr;  // quantiser absmax + non-finite flag
     bool smem_attr_set = false;
+    unsigned kv_attr_set = 0;      // attention kernels that may have their shared memory: a bit each
     unsigned char* xs_buf = nullptr;   // X pieces of the block-scaled path (calls without a plan)
     size_t xs_cap = 0;
     unsigned char* xh_buf = nullptr;   // prepared X of the exact path (calls without a plan)
@@ -1294,21 +1295,25 @@ tl_status launch_kv_commit(const tl::KvCommitParams& p, int page_tokens, cudaStr
 }
 
 template <int D, int NT>
-tl_status launch_kv_stream(const tl::KvAttnParams& p, cudaStream_t stream) {
+tl_status launch_kv_stream(const tl::KvAttnParams& p, DevState* d, cudaStream_t stream) {
     using C = tl::KvCfg<D, NT>;
-    TL_CUDA(cudaFuncSetAttribute(tl::kv_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES));
+    constexpr unsigned bit = 1u << (NT / 16 + (D == 128 ? 8 : 0));
+    if (!(__atomic_load_n(&d->kv_attr_set, __ATOMIC_RELAXED) & bit)) {
+        TL_CUDA(cudaFuncSetAttribute(tl::kv_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES));
+        __atomic_fetch_or(&d->kv_attr_set, bit, __ATOMIC_RELAXED);
+    }
     tl::kv_attention_kernel<D, NT><<<(unsigned)p.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(p);
     TL_CUDA(cudaGetLastError());
     return TL_OK;
 }
 
 template <int D>
-tl_status launch_kv_attention(const tl::KvAttnParams& p, cudaStream_t stream) {
-    tl_status st = p.nt == 16 ? launch_kv_stream<D, 16>(p, stream)
-                 : p.nt == 32 ? launch_kv_stream<D, 32>(p, stream)
-                 : p.nt == 48 ? launch_kv_stream<D, 48>(p, stream)
-                 : p.nt == 64 ? launch_kv_stream<D, 64>(p, stream)
-                              : launch_kv_stream<D, 80>(p, stream);
+tl_status launch_kv_attention(const tl::KvAttnParams& p, DevState* d, cudaStream_t stream) {
+    tl_status st = p.nt == 16 ? launch_kv_stream<D, 16>(p, d, stream)
+                 : p.nt == 32 ? launch_kv_stream<D, 32>(p, d, stream)
+                 : p.nt == 48 ? launch_kv_stream<D, 48>(p, d, stream)
+                 : p.nt == 64 ? launch_kv_stream<D, 64>(p, d, stream)
+                              : launch_kv_stream<D, 80>(p, d, stream);
     if (st != TL_OK) return st;
     const int chunks = (p.max_rows * p.group + tl::KV_MERGE_WARPS - 1) / tl::KV_MERGE_WARPS;
     const dim3 grid((unsigned)p.B, (unsigned)(p.heads * chunks));
@@ -1844,7 +1849,7 @@ tl_status tl_kv_attention(const void* q, long long q_stride, int n_q_heads, cons
     p.row_tiles = sp.row_tiles;
     p.nt = sp.nt;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return cache->head_dim == 128 ? launch_kv_attention<128>(p, s) : launch_kv_attention<64>(p, s);
+    return cache->head_dim == 128 ? launch_kv_attention<128>(p, d, s) : launch_kv_attention<64>(p, d, s);
 }
 
 tl_status tl_nvfp4_dequant(const void* w_codes, const void* w_scales, float global_scale, float* w_out, int N, int K,
