@@ -268,9 +268,9 @@ __device__ __forceinline__ uint32_t kv_moved(uint32_t w, float factor) {
 // scale, moves the bytes that the page holds already if the scale grew, and writes the new ones.
 // A page whose first token is written takes no notice of what it held. Bytes behind the run stay.
 // A page whose scale grows is read and written once more. For prompts the rows' bytes are the bound (bf16 in, E4M3 out:
-// 2 x 16k tokens of 8 heads take 42 us, 31 at copy speed), so the instructions an element are few: maxima and the test for
+// 2 x 16k tokens of 8 heads take 44 us, 31 at copy speed), so the instructions an element are few: maxima and the test for
 // infinities on packed halves, two channels of V a thread; 64 registers keep eight CTAs on an SM. For a few tokens it is
-// latency, two dependent reads (slots, rows) and the page's: 4 us.
+// latency, two dependent reads (slots, rows) and the page's: 5 us for 5 tokens.
 template <int D>
 __global__ void __launch_bounds__(KV_COMMIT_THREADS, 8) kv_commit_kernel(const KvCommitParams p) {
     constexpr int RP = D + 8;                     // padded row in elements: 16-byte column reads of 8 lanes spread over the banks

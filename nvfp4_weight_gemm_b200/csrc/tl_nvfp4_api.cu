@@ -1743,7 +1743,9 @@ tl_status tl_kv_commit(const tl_kv_cache* cache, const void* k, const void* v, l
     tl::KvCommitParams p{static_cast<uint8_t*>(cache->pages), cache->scales, static_cast<const __nv_bfloat16*>(k),
                          static_cast<const __nv_bfloat16*>(v), src, slots, d->err, row_stride, n_rows, n, cache->n_pages,
                          log2_of(cache->page_tokens), cache->n_kv_heads, 1};
-    // a few tokens: a CTA each, for latency; more: so many that some twelve CTAs an SM remain, up to a page's tokens
+    // a few tokens: a CTA each, for latency; more: so many that some twelve CTAs an SM remain, up to a page's tokens (a CTA
+    // for each token took 18.7 us for 64 requests of up to 16 tokens and 41 for 2,048 in a row, this 10.7 and 8.3; with four
+    // or twenty-four an SM the former is 12.4 or 12.5)
     {
         const long long each = (long long)n * 2 * cache->n_kv_heads / (12ll * d->num_sms);
         p.chunk = each < 1 ? 1 : each > cache->page_tokens ? cache->page_tokens : (int)each;
