@@ -454,6 +454,32 @@ def test_attention_sizes_of_scores_and_scales(q_size):
     c.check(c.run())
 
 
+def test_attention_weights_far_below_the_largest():
+    # The weight p vs of a token's bytes is held in f16, at 2^8 or more for the row's largest of a part (the reference lags it
+    # by up to 2^7, never leads): from 2^-22 of the largest down it is off by up to half a subnormal step, 2^-25 / 2^8 of the
+    # largest, whatever it is itself. That shows in channels where the bytes of the tokens with large weights are zero.
+    c = Case(31, [400], [5], 4, 2, 64, 16, spread=6.0, q_size=6.0)
+    c.scales[..., 0] = 2.0 ** -7
+    for page in range(len(c.pages)):
+        for h in range(2):
+            if c.scales[page, h, 1] > 2.0 ** -7:
+                for t in range(16):
+                    c.pages[page, h, 1][kv.place_v(t, np.arange(8), 64)] = 0
+    c.device()
+    out, weight, size, reach = c.reference()
+    largest = np.zeros((5, 4))
+    for i in range(5):
+        for h in range(4):
+            k = kv.cached(c.pages, c.scales, 16, 64, c.table[0], 400, h // 2, 0) @ c.qv[i, h] * c.scale
+            own = np.array([c.knv[j, h // 2] @ c.qv[i, h] * c.scale for j in range(5) if c.masks[i] >> j & 1])
+            top = max(k.max(), own.max())
+            vs = c.scales[c.table[0][np.arange(400) // 16], h // 2, 1].astype(np.float64)
+            largest[i, h] = (np.exp(k - top) * vs).max() / (np.exp(k - top).sum() + np.exp(own - top).sum())
+    off = 2.0 ** -11 + 4 * 2.0 ** -24 * (64 * size + 432) + 2.0 ** -19 + 2.0 ** -16.8 * reach
+    bar = 2.0 ** -8 * np.abs(out) + weight * off[..., None] + (400 * 448 * 2.0 ** -33 * largest)[..., None]
+    assert (np.abs(c.run().double().cpu().numpy() - out) <= bar).all()
+
+
 def test_attention_rows_of_very_different_sizes():
     # rows of one tree whose queries differ by 2^80 in size: each row's scores are as exact as alone
     c = Case(17, [300], [8], 4, 2, 64, 32)
