@@ -382,7 +382,8 @@ typedef struct {
  *   n_free      device int [1], in and out
  *   slots       device int [max_slots], output (max_slots >= 0)
  *   starts      device int [B + 1], output
- *   info        device int [4], output: {code, pages missing, slots missing, requests refused}
+ *   info        device int [4], output: {code, pages missing, slots missing, requests refused} (2^31 - 1 stands
+ *               for any larger number)
  * The code is 0, or a sum of: 1, the stack holds too few pages, and 2, max_slots is too small (in both
  * cases no request grows; returns still happen); 4, requests were refused (a negative length, or one
  * over table_width * page_tokens; they stay as they are); 8, the stack's height is negative or would

@@ -119,9 +119,22 @@ __global__ void __launch_bounds__(KV_SLOTS_THREADS, 1) kv_slots_kernel(const KvS
     const unsigned long long more = need > held ? need - held : 0, gone = held > need ? held - need : 0;
     unsigned long long adds, pages;
     const unsigned long long add_end = kv_block_scan(add, warp_sums, &adds);
-    const unsigned long long page_end = kv_block_scan(more | (gone << 32), warp_sums, &pages);
+    unsigned long long more_end, gone_end;
+    long long n_more, n_gone;
+    if ((long long)p.B * p.width <= 0xFFFFFFFFll) {
+        // both sums are of pages that the table has entries for, so 32 bits hold either: one scan for both
+        const unsigned long long page_end = kv_block_scan(more | (gone << 32), warp_sums, &pages);
+        more_end = page_end & 0xFFFFFFFFull;
+        gone_end = page_end >> 32;
+        n_more = (long long)(pages & 0xFFFFFFFFull);
+        n_gone = (long long)(pages >> 32);
+    } else {
+        more_end = kv_block_scan(more, warp_sums, &pages);
+        n_more = (long long)pages;
+        gone_end = kv_block_scan(gone, warp_sums, &pages);
+        n_gone = (long long)pages;
+    }
     const int n_refused = __syncthreads_count(refused);
-    const long long n_more = (long long)(pages & 0xFFFFFFFFull), n_gone = (long long)(pages >> 32);
     const bool corrupt = n_free < 0 || n_free + n_gone > p.n_pages;
     const long long top = n_free + n_gone;
     const long long pages_missing = n_more > top ? n_more - top : 0;
@@ -129,8 +142,8 @@ __global__ void __launch_bounds__(KV_SLOTS_THREADS, 1) kv_slots_kernel(const KvS
     const bool grows = !corrupt && pages_missing == 0 && slots_missing == 0;
     if (b < p.B) {
         pre_add[b] = grows ? (int)(add_end - add) : 0;
-        pre_more[b] = grows ? (int)((page_end & 0xFFFFFFFFull) - more) : 0;
-        pre_gone[b] = corrupt ? 0 : (int)((page_end >> 32) - gone);
+        pre_more[b] = grows ? (int)(more_end - more) : 0;
+        pre_gone[b] = corrupt ? 0 : (int)(gone_end - gone);
     }
     if (b == 0) {
         pre_add[p.B] = grows ? (int)adds : 0;
@@ -164,7 +177,7 @@ __global__ void __launch_bounds__(KV_SLOTS_THREADS, 1) kv_slots_kernel(const KvS
             p.starts[p.B] = pre_add[p.B];
             if (!corrupt) *p.n_free = (int)(top - pre_more[p.B]);
             p.info[0] = (corrupt ? 8 : 0) | (n_refused ? 4 : 0) | (slots_missing ? 2 : 0) | (pages_missing && !corrupt ? 1 : 0);
-            p.info[1] = corrupt ? 0 : (int)pages_missing;
+            p.info[1] = corrupt ? 0 : pages_missing > 0x7FFFFFFF ? 0x7FFFFFFF : (int)pages_missing;
             p.info[2] = slots_missing > 0x7FFFFFFF ? 0x7FFFFFFF : (int)slots_missing;
             p.info[3] = n_refused;
         }

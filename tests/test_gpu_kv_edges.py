@@ -1,0 +1,83 @@
+"""The 8-bit paged KV cache on the GPU at the edges of what its interface allows, against the plain statements in oracle/kv.py
+(bars: test_gpu_kv.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import nvfp4_weight_gemm_b200 as tl  # noqa: E402
+
+DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _init():
+    from nvfp4_weight_gemm_b200 import build
+    build.build()
+    tl.init(0)
+    yield
+    tl.check_device_error()
+
+
+def _i32(v):
+    return torch.tensor(np.asarray(v, np.int64).astype(np.int32), device=DEV)
+
+
+def _bf16(a):
+    """float array -> (bf16 tensor on the GPU, its values as float64)."""
+    t = torch.from_numpy(np.asarray(a, np.float32)).to(torch.bfloat16)
+    return t.to(DEV), t.to(torch.float64).numpy()
+
+
+# ---------------------------------------------------------------- block tables and slot maps
+
+def test_slots_of_a_table_with_more_than_2_to_32_entries():
+    # 1,024 requests x (2^22 + 1) pages: the sums of pages asked for, and of pages held, can pass 2^32
+    B, P, width = 1024, 16, 2 ** 22 + 1
+    table = torch.empty((B, width), dtype=torch.int32, device=DEV)
+    room = 200
+
+    def call(lens, want, head, free, n_free):
+        table[:, :8] = _i32(head)
+        df, dl, dn = _i32(free), _i32(lens), _i32([n_free])
+        s, st, info = (torch.full((n,), 123456, dtype=torch.int32, device=DEV) for n in (room, B + 1, 4))
+        tl.kv_slots(dl, _i32(want), table, df, dn, P, s, st, info)
+        torch.cuda.synchronize()
+        return [x.cpu().numpy() for x in (dl, table[:, :8], df, dn, s, st, info)]
+
+    free = np.arange(64) + 7
+    head = np.full((B, 8), -1)
+    full = width * P
+    # all ask for every page their row of the table has room for: nothing moves
+    got = call([0] * B, [full] * B, head, free, 5)
+    assert got[6].tolist() == [3, 2 ** 31 - 1, 2 ** 31 - 1, 0]
+    assert not got[0].any() and (got[1] == -1).all() and np.array_equal(got[2], free) and got[3][0] == 5
+    assert (got[4] == -1).all() and not got[5].any()
+    # all claim to hold such lengths and end, so that 2^32 + 5 pages would be returned to a stack for 64: nothing moves
+    lens = [full if b < 5 else full - P for b in range(B)]
+    got = call(lens, [0] * B, head, free, 5)
+    assert got[6].tolist() == [8, 0, 0, 0]
+    assert got[0].tolist() == lens and (got[1] == -1).all() and np.array_equal(got[2], free) and got[3][0] == 5
+    # ordinary lengths: as with a narrow table
+    rs = np.random.default_rng(1)
+    lens, want = rs.integers(0, 3, B) * (np.arange(B) % 40 == 3) * 30, np.zeros(B, int)
+    want[::90] = 9
+    want[3], want[83] = lens[3] + 20, lens[83] + 7
+    blocks = -(-lens // P)
+    ids = np.arange(int(blocks.sum()) + 40)
+    at = 0
+    for b in range(B):
+        head[b, : blocks[b]] = ids[at : at + blocks[b]]
+        at += blocks[b]
+    free = np.concatenate([ids[at:], np.full(at, 3)])
+    got, ref = call(lens, want, head, free, 40), kv.slots(lens, want, P, head, free, 40, room)
+    assert ref[6] == [0, 0, 0, 0] and (want < lens).any()
+    for x, y in zip(got, ref):
+        assert np.array_equal(np.ravel(x), np.ravel(y))
