@@ -406,8 +406,10 @@ tl_status tl_kv_slots(int* lens, const int* want, int B, int page_tokens, int* t
  *   k, v        device bf16 [n_rows][n_kv_heads][D], rows row_stride elements apart (slices of the QKV
  *               projection's output will do); 16-byte aligned, row_stride >= n_kv_heads * D, % 8 == 0
  *   src         NULL, or device int [n]: source rows, each in 0..n_rows-1
- *   slots       device int [n]; negative: the token goes nowhere. tl_kv_slots() writes them. No slot twice,
- *               and the slots of one page consecutive and ascending (else its bytes are undefined)
+ *   slots       device int [n]; negative: the token goes nowhere. tl_kv_slots() writes them. The tokens of one page
+ *               stand next to one another in the list, in ascending places without a gap: no token that goes
+ *               nowhere or to another page between them (src leaves rejected rows out), no slot twice. Else the
+ *               page's bytes and scales are undefined, for its tokens are then written by blocks that run at once
  *   n           0..2^24 (0 is a no-op); n_rows >= 1, and >= n without src
  * A slot outside the pool writes nothing and a row outside k and v counts as zeros; both set the device
  * status word (TL_ERR_DEVICE_FAULT at the next tl_check_device_error()). The pool may not overlap k, v,

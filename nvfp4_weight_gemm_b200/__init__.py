@@ -337,7 +337,9 @@ def kv_commit(cache, k, v, slots, src=None, stream=None):
     """Commit accepted tokens into the cache (tl_kv_commit): token i, row src[i] (or i) of k and v, goes to slots[i].
 
     k, v bf16 [rows, kv_heads, head_dim] (rows may be slices of the QKV projection's output); slots int32 [n] as
-    kv_slots() writes them (negative: nowhere); src int32 [n] or None. Returns `cache`."""
+    kv_slots() writes them (negative: nowhere); src int32 [n] or None. The tokens of one page must stand next to one another
+    in `slots`, in ascending places, with no negative slot or other page between them (else the page's contents are
+    undefined): rows that were not accepted are left out by `src`, not marked by -1. Returns `cache`."""
     index = cache._on_gpu()
     rows = _rows("k", k, cache.kv_heads, cache.head_dim, index)
     if not _same_rows(k, v) and _rows("v", v, cache.kv_heads, cache.head_dim, index) != rows:
