@@ -252,6 +252,14 @@ def _stream_of(index, stream):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+def _empty_on(stream, like, shape):
+    """An uninitialised tensor of like's type and device that belongs to `stream`: a block of the current stream's pool may
+    still be in use by what is queued there, for which `stream` does not wait."""
+    import torch
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape)
+
+
 def _call_on(index, fn, args):
     """fn(*args) with CUDA device `index` current."""
     import torch
@@ -373,7 +381,7 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
     cached tokens only). mask int32 [R]: bit j, the row sees node j of its request (None: the nodes up to itself).
     row_start int32 [B + 1]: request b has rows row_start[b]..row_start[b+1]-1, at most max_rows (<= 32) of them
     (None: R / B rows each). scale defaults to head_dim ** -0.5. out bf16 [R, q_heads, head_dim]; workspace uint8 of
-    kv_attention_workspace() bytes (both allocated when None). Returns `out`."""
+    kv_attention_workspace() bytes (both allocated when None, on the stream that the call runs on). Returns `out`."""
     import torch
     index, heads, dim, i32 = cache._on_gpu(), cache.kv_heads, cache.head_dim, torch.int32
     hq = q.shape[1] if q.dim() == 3 else -1
@@ -394,7 +402,10 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
         new_stride, k_ptr, v_ptr = new[1], k_new.data_ptr(), v_new.data_ptr()
     made = out is None
     if made:
-        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((R, hq, dim))
+        if stream is not None:
+            out = _empty_on(stream, q, (R, hq, dim))
+        else:
+            out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((R, hq, dim))
         out_stride = hq * dim
     else:
         n, out_stride = _rows("out", out, hq, dim, index)
@@ -402,10 +413,10 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
             _refuse("out must have q's rows")
     if R == 0:
         return out
-    own_workspace = workspace is None
-    if own_workspace:
+    if workspace is None:
         size = kv_attention_workspace(cache, hq, B, max_rows)
-        workspace = q.new_empty((size + 1) // 2)      # bf16, as q is: two bytes an element
+        n = (size + 1) // 2      # bf16, as q is: two bytes an element
+        workspace = q.new_empty(n) if stream is None else _empty_on(stream, q, n)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
         _refuse(f"workspace: need a contiguous uint8 tensor on cuda:{index}")
     else:
@@ -427,9 +438,6 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
              (q.data_ptr(), q_stride, hq, cache._c, table.data_ptr(), width, lens.data_ptr(), B, k_ptr, v_ptr, new_stride,
               mask_ptr, start_ptr, R, max_rows, dim ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, workspace.data_ptr(), size,
               _stream_of(index, stream)))
-    if stream is not None:   # what was allocated here for another stream than the current one
-        if made:
-            out.record_stream(stream)
-        if own_workspace:
-            workspace.record_stream(stream)
+    if made and stream is not None:   # the caller may use it on the current stream, after waiting for the other one
+        out.record_stream(torch.cuda.current_stream(index))
     return out

@@ -13,6 +13,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 import nvfp4_weight_gemm_b200 as tl  # noqa: E402
+from test_gpu_kv import Case  # noqa: E402
 
 DEV = torch.device("cuda:0")
 
@@ -81,3 +82,30 @@ def test_slots_of_a_table_with_more_than_2_to_32_entries():
     assert ref[6] == [0, 0, 0, 0] and (want < lens).any()
     for x, y in zip(got, ref):
         assert np.array_equal(np.ravel(x), np.ravel(y))
+
+
+# ---------------------------------------------------------------- attention
+
+def test_attention_on_another_stream_leaves_memory_that_the_current_one_still_uses():
+    # tensors of the sizes of the output and of the workspace are freed while a copy of them is still queued on the current
+    # stream: the call on the other stream, which does not wait for that copy, must not get their blocks
+    c = Case(24, [300, 9], [4, 2], 4, 2, 128, 32).device()
+    good = c.run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    size = tl.kv_attention_workspace(c.cache, 4, 2, 4)
+    for _ in range(3):
+        shapes = [good.shape, ((size + 1) // 2,)]
+        held = [torch.full(s, 7.0 + i, dtype=torch.bfloat16, device=DEV) for i, s in enumerate(shapes)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(30_000_000)
+        copies = [t.clone() for t in held]
+        del held
+        y = tl.kv_attention(c.dq, c.cache, c.dtable, c.dlens, c.dkn, c.dvn, mask=c.dmask, row_start=c.dstart, max_rows=4, stream=side)
+        side.synchronize()
+        z = y.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(y, good) and torch.equal(z, good)
+        for i, t in enumerate(copies):
+            assert (t == 7.0 + i).all()
