@@ -290,7 +290,7 @@ __device__ __forceinline__ uint32_t kv_moved(uint32_t w, float factor) {
 template <int D>
 __global__ void __launch_bounds__(KV_COMMIT_THREADS, 8) kv_commit_kernel(const KvCommitParams p) {
     constexpr int RP = D + 8;                     // padded row in elements: 16-byte column reads of 8 lanes spread over the banks
-    extern __shared__ __nv_bfloat16 rows[];       // [P][RP]
+    extern __shared__ __align__(16) __nv_bfloat16 rows[];      // [P][RP], in 16-byte pieces
     __shared__ int sl[2 * KV_COMMIT_THREADS];     // slots of tokens i0 - 1 .. i0 + chunk + P - 2, all that a run may reach
     __shared__ unsigned begins[4];                // bit i of word i / 32: a run begins at token i of the chunk
     __shared__ unsigned tops[4];
