@@ -1174,7 +1174,8 @@ __global__ void __launch_bounds__(KV_MERGE_THREADS) kv_merge_kernel(const KvAttn
         }
         const float s = sees ? ((acc[0] + acc[1]) + (acc[2] + acc[3])) * p.scale : -INFINITY;
         m = kv_warp_max(s);
-        const float pr = sees ? exp2f(s - m) : 0.0f;
+        // where every node's score is minus infinity they weigh nothing beside cached tokens; alone they leave 0 / 0
+        const float pr = sees ? exp2f(s - ((m == -INFINITY && rq.len > 0) ? 0.0f : m)) : 0.0f;
         l = pr;
 #pragma unroll
         for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);

@@ -109,3 +109,19 @@ def test_attention_on_another_stream_leaves_memory_that_the_current_one_still_us
         assert torch.equal(y, good) and torch.equal(z, good)
         for i, t in enumerate(copies):
             assert (t == 7.0 + i).all()
+
+
+@pytest.mark.parametrize("n", [0, 1, 40, 300])
+def test_attention_own_nodes_whose_score_is_minus_infinity(n):
+    # a score of minus infinity is a weight of zero: beside cached tokens or nodes with finite scores it changes nothing, and
+    # alone it leaves 0 / 0
+    c = Case(27, [n], [4], 4, 2, 64, 16, masks=[0x1, 0x2, 0x6, 0xC])
+    c.q[:, :, 3] = -0.1 - np.abs(c.q[:, :, 3])
+    c.kn[:3, :, 3] = np.inf
+    c.device()
+    y = c.run().double()
+    c.masks = np.array([0x0, 0x0, 0x0, 0x8])        # the nodes whose scores are finite
+    if n == 0:
+        assert torch.isnan(y[:3]).all()
+        y[:3] = 0.0
+    c.check(y)
