@@ -125,3 +125,46 @@ def test_attention_own_nodes_whose_score_is_minus_infinity(n):
         assert torch.isnan(y[:3]).all()
         y[:3] = 0.0
     c.check(y)
+
+
+@pytest.mark.parametrize("at", [0, 4100, 8191])
+@pytest.mark.parametrize("apart", [5, 12])
+def test_attention_sink_beside_a_tail_that_weighs_a_quarter(at, apart):
+    # One token's score is 10 above those of 8,191 others, whose small weights add up to a quarter of the sum; the scale of V in
+    # the sink's page is 2^5 or 2^12 times the others', so the weights of their bytes are 2^-19 or 2^-26 of the sink's: in f16 without
+    # the shift by 2^8 they would be subnormal, or zero. In half of the channels the sink's V is zero and the tail's has one sign,
+    # so that a result without the tail's V is off by all of it there; one without the tail's weights in the sum is off by a third
+    # elsewhere. 296 requests share the pages, so that a block's share of the work is two whole requests and the tail stands behind
+    # the sink's reference. The bar has one more term: a weight is held to half a subnormal step of f16, 2^-25, at 2^8 for the largest.
+    P, n, B = 64, 8192, 296
+    c = Case(28, [n], [1], 1, 1, 64, P, new=False)
+    rs = c.rs
+    page = int(c.table[0, at // P])
+    c.scales[..., 0], c.scales[..., 1] = 2.0 ** -5, 2.0 ** (-7 - apart)
+    c.scales[page, 0, 1] = 2.0 ** -7
+    c.q[:] = 0.0
+    c.q[0, 0, 0], c.q[0, 0, 1] = 8.0, 0.25
+    v = rs.normal(0, 60, c.pages[:, 0, 1].shape).reshape(-1, P // 16, 64, 16)
+    v[:, :, :32] = np.abs(v[:, :, :32]) + 20.0
+    v[page] /= 2.0 ** min(apart, 8)                                   # the tail's tokens beside the sink
+    k = rs.normal(0, 60, c.pages[:, 0, 0].shape).reshape(-1, 4, P, 16)
+    k[:, 0, :, 0] = 0.0
+    k[page, 0, at % P, 0] = 320.0                                     # s = 8 * 320 / 32 / 8 = 10
+    v[page, at % P // 16, :32, at % 16], v[page, at % P // 16, 32:, at % 16] = 0.0, 3.0
+    c.pages[:, 0, 0], c.pages[:, 0, 1] = (kv.e4m3_bytes(x).reshape(len(x), -1) for x in (k, v))
+    c.device()
+    out, weight, size, reach = c.reference()
+    kc, vc = (kv.cached(c.pages, c.scales, P, 64, c.table[0], n, 0, side) for side in (0, 1))
+    s = c.scale * (kc @ c.qv[0, 0])
+    p = np.exp(s - s.max())
+    own, vs = c.scales[c.table[0][np.arange(n) // P], 0, 1, None].astype(np.float64), float(c.scales[page, 0, 1])
+    off = 2.0 ** -11 + 4 * 2.0 ** -24 * (64 * size + n) + 2.0 ** -19 + 2.0 ** -16.8 * reach
+    bar = (2.0 ** -8 * np.abs(out) + weight * off[..., None])[0, 0] + 2.0 ** -33 * vs * np.abs(vc / own).sum(0) / p.sum()
+    # what the tail is to the result, on the host
+    assert s.argmax() == at and 0.2 < 1 - p[at] / p.sum() < 0.3
+    assert np.median(p * own[:, 0]) < 2.0 ** (-14 - apart) * vs
+    without_v, without_l = p[at] * vc[at] / p.sum(), p @ vc / p[at]
+    assert (np.abs(without_v - out[0, 0]) > 8 * bar)[:32].all() and (np.abs(without_l - out[0, 0]) > 8 * bar).all()
+    y = tl.kv_attention(c.dq.expand(B, 1, 64).contiguous(), c.cache, _i32(np.tile(c.table, (B, 1))), _i32([n] * B), scale=c.scale)
+    torch.cuda.synchronize()
+    assert (np.abs(y[:, 0].double().cpu().numpy() - out[0, 0]) <= bar).all()
