@@ -442,9 +442,10 @@ tl_status tl_kv_attention_workspace(const tl_kv_cache* cache, int n_q_heads, int
  * All of q, k_new, v_new and out: 16-byte aligned, strides multiples of 8 that hold a row.
  * n_q_heads is a multiple of n_kv_heads, at most TL_KV_MAX_GROUP times it; B in 1..TL_KV_MAX_BATCH;
  * B * n_kv_heads * (row tiles of 80) * (9 * table tokens / 128 + 16) at most 4e9 (TL_ERR_UNSUPPORTED beyond).
- * Accuracy: sums are fp32. Cached K counts with its bytes and q to 2^-17 of its row's largest element; a cached token's weight
- * (its share of the softmax times the page's V scale) is rounded to f16, 2^-11 of it, and weights under 2^-22 of the row's
- * largest to 2^-33 of that one. out is rounded to bf16.
+ * Accuracy: sums are fp32; those of values of one sign lose up to 2^-11 of themselves, however long the context is. Cached K
+ * counts with its bytes and q to 2^-17 of its row's largest element; a cached token's weight (its share of the softmax times
+ * the page's V scale) is rounded to f16, 2^-11 of it, and weights under 2^-22 of the row's largest to 2^-33 of that one. out
+ * is rounded to bf16.
  * A page id outside the pool is read as page 0, and a request whose rows do not fit R or max_rows is left
  * out; both set the device status word. The order of all sums is fixed: equal calls give equal bits.
  * Asynchronous on `stream`; nothing is allocated once tl_init() ran. */

@@ -36,6 +36,11 @@
 namespace tl {
 
 constexpr int KV_TILE = 128;          // cached tokens of a tile
+// Tiles of a segment at most. The MMA truncates each product against its accumulator, so that sums of values of one sign lose
+// some 2^-27 of themselves a token: 0.65% over 2^20 tokens in one accumulator, 2.5% over 2^22. Over 2^16 it is 2^-11, and what
+// follows is added to the part in fp32 by the softmax warps. (4 requests of 2^20 tokens with trees of 32 rows: 4.73 ms, as with one
+// segment a part; with 256 tiles 4.79.)
+constexpr int KV_SEG_TILES = 512;
 constexpr int KV_MAX_ROWS = 32;       // rows of one request: the bits of a mask
 constexpr float KV_LOG2E = 1.4426950408889634f;
 
@@ -114,10 +119,11 @@ struct KvShares {
     __device__ __forceinline__ int owner(unsigned x) const { return x < r * (q + 1) ? (int)(x / (q + 1)) : (int)(r + (x - r * (q + 1)) / q); }
 };
 
-// One step of a walk along a range of the tile list: tiles k0..k1 of row tile rt of (b, head).
+// One step of a walk along a range of the tile list: tiles k0..k1 of row tile rt of (b, head), KV_SEG_TILES of them at most.
 struct __align__(16) KvSeg {
     int b, head, rt, k0, k1, nt, n_rows;
-    int valid;      // tokens of its last tile (128 unless it is the unit's last)
+    short valid;    // tokens of its last tile (128 unless it is the unit's last)
+    short more;     // to be added to the unit's part, which the segments in front of it began
 };
 
 struct KvWalk {
@@ -129,6 +135,7 @@ struct KvWalk {
     int b, head, rt, k;      // next: tile k of unit (b, head, rt)
     int tiles;               // of request b
     unsigned at;             // where its unit begins
+    bool more;               // some of its unit's tiles went out in the segment in front
     KvShape s;
     __device__ __forceinline__ void look() {
         tiles = kv_tiles(len[b]);
@@ -137,7 +144,7 @@ struct KvWalk {
     __device__ __forceinline__ KvWalk(const KvAttnParams& p, const unsigned* pre_, const int* len_, const uint8_t* rows_, unsigned begin,
                                       unsigned end_, int most_)
         : pre(pre_), len(len_), rows(rows_), B(p.B), heads(p.heads), group(p.group), most(most_), end(end_), b(p.B), head(0), rt(0), k(0),
-          tiles(0), at(0) {
+          tiles(0), at(0), more(false) {
         if (begin >= end) return;
         int lo = 0, hi = B;
 #pragma unroll 1
@@ -169,7 +176,7 @@ struct KvWalk {
     }
     __device__ __forceinline__ bool next(KvSeg& g) {
         if (b >= B || at >= end) return false;
-        const int k1 = s.tile_from(end - at, tiles);
+        const int k1 = min(s.tile_from(end - at, tiles), k + KV_SEG_TILES);
         if (k1 <= k) return false;
         g.b = b;
         g.head = head;
@@ -178,9 +185,11 @@ struct KvWalk {
         g.k1 = k1;
         g.nt = s.nt;
         g.n_rows = min((int)rows[b] * group - rt * s.nt, s.nt);
-        g.valid = k1 == tiles ? ((len[b] - 1) & (KV_TILE - 1)) + 1 : KV_TILE;
+        g.valid = (short)(k1 == tiles ? ((len[b] - 1) & (KV_TILE - 1)) + 1 : KV_TILE);
+        g.more = more;
         k = k1;
-        if (k == tiles) step();
+        more = k != tiles;
+        if (!more) step();
         return true;
     }
 };
@@ -1040,25 +1049,54 @@ __global__ void __launch_bounds__(KvCfg<D, NT>::THREADS, 1) kv_attention_kernel(
             }
             const size_t slot = (((size_t)sg.b * p.heads + sg.head) * p.row_tiles + sg.rt + g) * NT;
             kv_group_sync(bar_id);
-            {
-                const int row = c0 + t;
+            const int row = c0 + t;
+            if (!sg.more) {
                 if (t < 8 * nb && row < sg.n_rows) {
                     const float* const rd = g_red + t;
                     p.part_ml[slot + row] = make_float2(-g_negm[t] - KV_P_SHIFT, 256.0f * ((rd[0] + rd[NH]) + (rd[2 * NH] + rd[3 * NH])));
                 }
-            }
-            wait(ofull, seg & 1u);
-            tc_fence_after();
+                wait(ofull, seg & 1u);
+                tc_fence_after();
 #pragma unroll 1
-            for (int j = 0; j < nb; ++j) {
-                float o[8];
-                tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0) + 8 * j, o);
-                tmem_wait_ld();
-                if (D == 128 || qd < 2) {
-                    float* const to = p.part_o + (slot + 8 * j + c0) * D + t;
+                for (int j = 0; j < nb; ++j) {
+                    float o[8];
+                    tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0) + 8 * j, o);
+                    tmem_wait_ld();
+                    if (D == 128 || qd < 2) {
+                        float* const to = p.part_o + (slot + 8 * j + c0) * D + t;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (8 * j + c0 + i < sg.n_rows) to[i * D] = o[i];
+                        for (int i = 0; i < 8; ++i)
+                            if (8 * j + c0 + i < sg.n_rows) to[i * D] = o[i];
+                    }
+                }
+            } else {
+                // joined with what these threads have written of the part; where an m is minus infinity there is nothing to join,
+                // but a NaN counts
+                if (t < 8 * nb && row < sg.n_rows) {
+                    const float* const rd = g_red + t;
+                    const float2 had = p.part_ml[slot + row];
+                    const float m = -g_negm[t] - KV_P_SHIFT, top = fmaxf(had.x, m);
+                    const float f0 = (had.x == -INFINITY) ? 0.0f : kv_ex2(had.x - top), f1 = (m == -INFINITY) ? 0.0f : kv_ex2(m - top);
+                    p.part_ml[slot + row] = make_float2(top, had.y * f0 + 256.0f * ((rd[0] + rd[NH]) + (rd[2 * NH] + rd[3 * NH])) * f1);
+                    g_resc[t] = f0;
+                    g_negm[t] = f1;
+                }
+                kv_group_sync(bar_id);
+                wait(ofull, seg & 1u);
+                tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < nb; ++j) {
+                    float o[8], had[8];
+                    float* const to = p.part_o + (slot + 8 * j + c0) * D + t;
+                    tmem_ld8(t_lane + (uint32_t)(C::O_COL + c0) + 8 * j, o);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) had[i] = ((D == 128 || qd < 2) && 8 * j + c0 + i < sg.n_rows) ? to[i * D] : 0.0f;
+                    tmem_wait_ld();
+                    if (D == 128 || qd < 2) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (8 * j + c0 + i < sg.n_rows) to[i * D] = fmaf(had[i], g_resc[8 * j + i], o[i] * g_negm[8 * j + i]);
+                    }
                 }
             }
             tc_fence_before();

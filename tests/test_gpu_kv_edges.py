@@ -168,3 +168,87 @@ def test_attention_sink_beside_a_tail_that_weighs_a_quarter(at, apart):
     y = tl.kv_attention(c.dq.expand(B, 1, 64).contiguous(), c.cache, _i32(np.tile(c.table, (B, 1))), _i32([n] * B), scale=c.scale)
     torch.cuda.synchronize()
     assert (np.abs(y[:, 0].double().cpu().numpy() - out[0, 0]) <= bar).all()
+
+
+def test_attention_sums_of_a_long_context_keep_their_bits():
+    # 148 requests of 2^22 tokens (one page again and again) whose V has one sign: a block adds up a whole request. The MMA cuts off
+    # each product at its accumulator's last bit, at most 2^-23 of it, and one accumulator takes 2^16 products: at most 2^-7 of W. A
+    # thread adds up 2^9 weights below, each sum within 2^-24: 2^-14 with the joining of the parts.
+    P, D, n, B = 128, 64, 2 ** 22, 148
+    c = Case(29, [P], [1], 1, 1, D, P, new=False, extra_pages=0)
+    c.scales[:] = 2.0 ** -6
+    c.pages[:, :, 1] &= 0x7F
+    c.device()
+    out, weight, size, reach = c.reference()
+    off = 2.0 ** -7 + 2.0 ** -14 + 2.0 ** -11 + 4 * 2.0 ** -24 * D * size + 2.0 ** -19 + 2.0 ** -16.8 * reach
+    bar = 2.0 ** -8 * np.abs(out) + weight * off[..., None]
+    y = tl.kv_attention(c.dq.expand(B, 1, D).contiguous(), c.cache, torch.full((B, n // P), int(c.table[0, 0]), dtype=torch.int32, device=DEV),
+                        torch.full((B,), n, dtype=torch.int32, device=DEV), scale=c.scale)
+    torch.cuda.synchronize()
+    assert (np.abs(y.double().cpu().numpy() - out) <= bar).all()
+
+
+@pytest.mark.parametrize("D,hq,hkv,rows,B,times", [(64, 2, 2, 1, 50, 200), (128, 10, 2, 32, 12, 160), (64, 16, 4, 3, 30, 90), (128, 4, 4, 9, 40, 70)])
+def test_attention_blocks_that_join_many_parts_of_a_request(D, hq, hkv, rows, B, times):
+    # contexts of `times` times the same 4,000 tokens, of which a block takes several times what one accumulator takes, beside short
+    # ones; the weights are those of the 4,000 tokens. Scales of V far apart, so that the parts' references differ.
+    P, n = 16, 4000
+    c = Case(30 + rows, [n], [rows], hq, hkv, D, P, new=False, spread=3.0, q_size=2.0, extra_pages=0)
+    c.scales[..., 0] = 2.0 ** -6
+    c.device()
+    out, weight, size, reach = c.reference()
+    off = 2.0 ** -7 + 2.0 ** -14 + 2.0 ** -11 + 4 * 2.0 ** -24 * D * size + 2.0 ** -19 + 2.0 ** -16.8 * reach
+    # the weights' own limit, as where they are far below the largest: half a subnormal step of f16, 2^-25, at 2^8 for the largest
+    small = np.zeros(out.shape)
+    for h in range(hkv):
+        k, v = (kv.cached(c.pages, c.scales, P, D, c.table[0], n, h, side) for side in (0, 1))
+        vs = c.scales[c.table[0][np.arange(n) // P], h, 1].astype(np.float64)
+        for i in range(rows):
+            for a in range(h * (hq // hkv), (h + 1) * (hq // hkv)):
+                p = np.exp(c.scale * (k @ c.qv[i, a]) - (c.scale * (k @ c.qv[i, a])).max())
+                small[i, a] = 2.0 ** -33 * (p * vs).max() * np.abs(v / vs[:, None]).sum(0) / p.sum()
+    bar = 2.0 ** -8 * np.abs(out) + weight * off[..., None] + small
+    few = [1 if b % 5 == 2 else times for b in range(B)]
+    table = np.full((B, times * n // P), -1)
+    for b in range(B):
+        table[b, : few[b] * n // P] = np.tile(c.table[0, : n // P], few[b])
+    args = (c.dq.repeat(B, 1, 1), c.cache, _i32(table), _i32([f * n for f in few]))
+    y = tl.kv_attention(*args, scale=c.scale)
+    torch.cuda.synchronize()
+    got = y.double().cpu().numpy().reshape(B, rows, hq, D)
+    assert (np.abs(got - out) <= bar).all()
+    assert torch.equal(y, tl.kv_attention(*args, scale=c.scale))
+
+
+def test_attention_nan_in_one_part_of_a_block_reaches_the_row():
+    # NaN in a token of the first, of a middle and of the last of the parts that a block joins
+    P, D, n, B = 128, 64, 128 * 1400, 148
+    c = Case(31, [3 * P], [1], 1, 1, D, P, new=False, extra_pages=0).device()
+    ids = [int(x) for x in c.table[0, :3]]
+    c.cache.pages[ids[1], 0, 0, 0] = 0x7F                                     # K
+    c.cache.pages[ids[2], 0, 1].view(P // 16, D, 16)[0, 5, 0] = 0x7F          # V, channel 5
+    table = np.full((B, n // P), ids[0])
+    at = {3: (0, 1), 9: (600, 1), 20: (1399, 1), 31: (10, 2), 40: (800, 2), 60: (1398, 2)}
+    for b, (j, which) in at.items():
+        table[b, j] = ids[which]
+    y = tl.kv_attention(c.dq.expand(B, 1, D).contiguous(), c.cache, _i32(table), _i32([n] * B), scale=c.scale)[:, 0].float().cpu().numpy()
+    for b in range(B):
+        j, which = at.get(b, (0, 0))
+        bad = np.isnan(y[b])
+        assert bad.all() if which == 1 else bad[5] and bad.sum() == 1 if which == 2 else not bad.any()
+
+
+def test_attention_of_one_request_for_seconds():
+    # 2^30 - 128 tokens, 52 heads, all in one page: the longest call there is. Scores are all zero and V is one value a channel, so
+    # every sum is exact.
+    H, D, P, width = 52, 64, 128, 2 ** 23 - 1
+    cache = tl.KvCache(torch.zeros((1, H, 2, P * D), dtype=torch.uint8, device=DEV), torch.full((1, H, 2), 0.125, device=DEV), P)
+    v = cache.pages[0, :, 1].view(H, P // 16, D, 16)
+    v[:, :, :, :] = 0x38                            # 1.0
+    v[:, :, 3::5] = 0xC4                            # -3.0
+    want = torch.full((D,), 0.125, device=DEV)
+    want[3::5] = -0.375
+    q = torch.randn((1, H, D), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(torch.bfloat16)
+    y = tl.kv_attention(q, cache, torch.zeros((1, width), dtype=torch.int32, device=DEV), _i32([width * P]))
+    tl.check_device_error()
+    assert (y.float() == want).all()
