@@ -381,7 +381,9 @@ def kv_attention(q, cache, table, lens, k_new=None, v_new=None, mask=None, row_s
     cached tokens only). mask int32 [R]: bit j, the row sees node j of its request (None: the nodes up to itself).
     row_start int32 [B + 1]: request b has rows row_start[b]..row_start[b+1]-1, at most max_rows (<= 32) of them
     (None: R / B rows each). scale defaults to head_dim ** -0.5. out bf16 [R, q_heads, head_dim]; workspace uint8 of
-    kv_attention_workspace() bytes (both allocated when None, on the stream that the call runs on). Returns `out`."""
+    kv_attention_workspace() bytes (both allocated when None, on the stream that the call runs on). Rows of no request, and
+    those of a request whose offsets do not fit, are left as they are in `out`: uninitialised, where it is allocated here.
+    Returns `out`."""
     import torch
     index, heads, dim, i32 = cache._on_gpu(), cache.kv_heads, cache.head_dim, torch.int32
     hq = q.shape[1] if q.dim() == 3 else -1

@@ -228,13 +228,14 @@ struct KvWalk {
 //   * warps 8..15   softmax: two groups of four warps, half of the blocks of 8 rows each, lane = token; blocks without
 //                   rows are passed over. A group also reads its rows of O (lane = channel) when a segment ends and writes
 //                   the part.
-// Bound: for a few rows the cache's bytes (64 requests of up to 8k tokens, 8 KV heads of 128, one row each: 106 us, 80% of
+// Bound: for a few rows the cache's bytes (64 requests of up to 8k tokens, 8 KV heads of 128, one row each: 107 us, 80% of
 // what a copy reaches). A tile of 128 tokens and 128 channels takes 0.82 us with 16 rows, 1.17 with 48 and 1.72 with 80, of
-// which memory needs 0.74. With many rows it is the softmax's: its warps are busy all the time, one step after another (a
-// thread's 40 scores of a tile: 150 ns of load and wait for them, 250 of scale and maximum, 100 of vote, 250 to 400 of
-// exponentials, 70 of fence and arrival, 130 of the next tile's wait), and no unit is busy half the time. Rows as operand A,
-// padded to 128 and a row a thread (no votes, no exchange across lanes), took 1.81; the groups on alternate tiles, four groups
-// on two tiles, or three groups on thirds of the rows 1.99 and more.
+// which memory needs 0.74. With many rows it is the softmax's: its warps go through one step after another, and no unit is busy
+// half the time. In cycles of a tile of 80 rows (of 40), by time stamps in the kernel, two groups' average: 280 (170) of wait for
+// the scores, 470 (340) of their load, 510 (300) of scale and maximum, 230 (150) of vote, 185 (105) until the weights, 720 (550)
+// of exponentials and weights, 160 (95) of fence and arrival, 250 (280) until the next wait: 2,800 (2,000) of the 2,910 (2,040)
+// that such a tile takes with the stamps. Rows as operand A, padded to 128 and a row a thread (no votes, no exchange across
+// lanes), took 1.81 us; the groups on alternate tiles, four groups on two tiles, or three groups on thirds of the rows 1.99 and more.
 // Every mbarrier wait is bounded; after one has run out the others return at once, every role runs to its end
 // (so no named barrier is left waiting), and the status word is set.
 
@@ -253,7 +254,7 @@ struct KvCfg {
     static constexpr int QSTEPS = 2 * D / 32;                  // MMAs of S^T: 32 channels each, both terms
     static constexpr int Q_BYTES = NT * D * 2;                 // slabs of [NT] 128-byte rows, swizzled: the first terms, the second
     static constexpr int P_BYTES = NT * KV_TILE * 2;
-    // tiles in flight between converters, MMAs and softmax: what tensor memory (and for 80 rows shared memory) holds
+    // tiles in flight between movers, MMAs and softmax: what tensor memory holds
     static constexpr int PER_TILE = D / 4 + KV_TILE / 2 + NT;
     static constexpr int BUFS = (4 * PER_TILE + NT <= 512) ? 4 : (3 * PER_TILE + NT <= 512) ? 3 : 2;
     // S^T runs up to BUFS tiles (so perhaps BUFS segments) ahead of the softmax, and Q two segments ahead of S^T
@@ -389,8 +390,8 @@ __device__ __forceinline__ void kv_decode16(uint4 q, uint32_t* out) {
             : "=r"(out[2 * j]), "=r"(out[2 * j + 1]) : "r"(w[j]));
 }
 
-// Bounded wait that also gives up when another role has aborted the CTA. A poll may sleep in hardware for some 20
-// microseconds: the limit is seconds, far beyond any launch.
+// Bounded wait that also gives up when another role has aborted the CTA. A poll sleeps in hardware for some 4 microseconds,
+// so the limit is about a second: no wait lasts longer than a segment, 0.9 ms.
 __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
 #pragma unroll 1
     for (uint32_t i = 0; i < (TL_WAIT_LIMIT >> 4); ++i) {

@@ -282,7 +282,7 @@ __device__ __forceinline__ uint32_t kv_moved(uint32_t w, float factor) {
 // A page whose first token is written takes no notice of what it held. Bytes behind the run stay.
 // A page has one run in a call: the caller keeps its tokens together. (Two runs of a page, with tokens that go nowhere between
 // them, would change one scale from two CTAs. A search of the list for them, so that one CTA writes them in turn, was right but
-// cost calls without any: 2.8 -> 3.2 us for 5 tokens, 43 -> 47 to 56 for 2 x 16k.)
+// cost calls without any: 2.8 -> 3.2 us for 5 tokens, replayed back to back, 43 -> 47 to 56 for 2 x 16k.)
 // A page whose scale grows is read and written once more. For prompts the rows' bytes are the bound (bf16 in, E4M3 out:
 // 2 x 16k tokens of 8 heads take 44 us, 31 at copy speed), so the instructions an element are few: maxima and the test for
 // infinities on packed halves, two channels of V a thread; 64 registers keep eight CTAs on an SM. For a few tokens it is
